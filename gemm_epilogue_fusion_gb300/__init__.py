@@ -74,6 +74,11 @@ SIGNATURES = {
                                      _vp, _fp, _vp, _fp, _i64, _i64, _i64, _i64, _vp, _vp]),
     "coda_block_rowscale_fp8": (_i32, [_vp, _fp, _vp, _fp, _vp, _fp, _vp, _vp, _fp, _f32, _vp, _fp, _fp, _fp, _vp, _fp,
                                        _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "coda_paged_append": (_i32, [_vp] * 7 + [_i64] * 8 + [ctypes.c_double, _i32, _i32, _fp, _fp, _vp]),
+    "coda_paged_attention_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "coda_paged_attention": (_i32, [_vp, _i64] + [_vp] * 7 + [_i64] * 8 + [_f32, _i32, _i32, _fp, _fp, _vp, _vp]),
+    "coda_logprobs": (_i32, [_vp, _i64, _vp, _fp, _fp, _fp, _fp, _vp, _i64, _i64, _i64, _i32, _vp]),
+    "coda_logprobs_backward": (_i32, [_vp, _i64, _vp, _fp, _fp, _fp, _fp, _vp, _i64, _i64, _i64, _i32, _vp]),
     "coda_amax": (_i32, [_vp, _i64, _i32, _fp, _vp]),
     "coda_quantize_e4m3": (_i32, [_vp, _i64, _i32, _fp, _vp, _fp, _vp]),
     "coda_selftest_wait_timeout": (_i32, [_i64, _vp]),
@@ -645,6 +650,175 @@ def coda_block_rowscale_fp8(A, amax_a, W1t, scale_w1, R, W2t, scale_w2, eps: flo
                                        _dev(scale_h, "scale_h"), _dev(Z, "Z"), M, N, K, N2,
                                        _dev(workspace, "workspace"), _stream(src, stream)))
     return {"Aq": Aq, "scale_a": scale_a, "h": H, "P": P, "amax_h": amax_h, "Hq": Hq, "scale_h": scale_h, "Z": Z}
+
+
+_I32 = (torch.int32,)
+
+
+def _cache_shape(k_cache, v_cache, dtype):
+    """(num_pages, kv_heads, page_size, head_dim, cache dtype code) of a pair of caches for rows of `dtype`."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache has {k_cache.dim()} dimensions, expected [num_pages, kv_heads, page_size, head_dim]")
+    _want(k_cache, "k_cache", dtypes=(dtype,) + (_BYTE if dtype == torch.bfloat16 else ()))
+    _want(v_cache, "v_cache", k_cache.shape, (k_cache.dtype,))
+    return (*k_cache.shape, _dtype_code(k_cache))
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(device pointer, row stride in elements) of a CUDA matrix [M, N], or
+    [M, heads, head_dim] with contiguous heads, whose rows may lie further
+    apart than they are wide."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if t.is_contiguous():
+        return _dev(t, name), t[0].numel() if t.shape[0] else t.numel()
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != inner:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        inner *= n
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr() or None, t.stride(0) if t.shape[0] > 1 else inner
+
+
+def coda_paged_append(Z, positions, page_table, k_cache, v_cache, q_heads: int, *, row_seq=None, base: float = 0.0,
+                      Q=None, want_q: bool = True, scale_k=None, scale_v=None, stream=None):
+    """Writes K (rotated) and V of the QKV rows Z [M, (q_heads + 2 kv_heads) head_dim] to the paged caches
+    [num_pages, kv_heads, page_size, head_dim] (changed in place) at ``positions`` [M] int32 of the rows' sequences
+    (``row_seq`` [M] int32, else row i is sequence i of ``page_table`` [num_seqs, max_pages] int32).  ``base`` 0: Z is
+    already rotated.  Rows with a negative position are left out.  Returns the rotated queries [M, q_heads, head_dim],
+    or None with ``want_q=False``."""
+    lib = load_library()
+    M = Z.shape[0]
+    code = _dtype_code(Z)
+    pages, kv_heads, page_size, D, ccode = _cache_shape(k_cache, v_cache, Z.dtype)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has {page_table.dim()} dimensions, expected [num_seqs, max_pages]")
+    _want(Z, "Z", (M, (q_heads + 2 * kv_heads) * D), (torch.float32, torch.bfloat16))
+    _want(positions, "positions", (M,), _I32)
+    _want(page_table, "page_table", dtypes=_I32)
+    _want(row_seq, "row_seq", (M,), _I32)
+    _want_scalars(scale_k=scale_k, scale_v=scale_v)
+    if Q is None and want_q:
+        Q = torch.empty(M, q_heads, D, dtype=Z.dtype, device=Z.device)
+    if Q is not None:
+        _want(Q, "Q", (M, q_heads, D), (Z.dtype,))
+    _check(lib.coda_paged_append(_dev(Z, "Z"), _dev(positions, "positions"), _dev(row_seq, "row_seq"),
+                                 _dev(page_table, "page_table"), _dev(Q, "Q"), _dev(k_cache, "k_cache"),
+                                 _dev(v_cache, "v_cache"), M, page_table.shape[0], page_table.shape[1], q_heads,
+                                 kv_heads, D, pages, page_size, float(base), code, ccode, _dev(scale_k, "scale_k"),
+                                 _dev(scale_v, "scale_v"), _stream(Z, stream)))
+    return Q
+
+
+def coda_paged_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load_library().coda_paged_attention_workspace_bytes(q_heads, kv_heads, head_dim))
+
+
+def paged_attention_workspace(q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A zeroed workspace for coda_paged_attention, for any number of rows (calls leave it ready for the next)."""
+    n = coda_paged_attention_workspace_bytes(q_heads, kv_heads, head_dim)
+    if n < 0:
+        raise ValueError(f"q_heads = {q_heads}, kv_heads = {kv_heads}, head_dim = {head_dim} out of range")
+    return torch.zeros((n + 3) // 4, dtype=torch.int32, device=device)
+
+
+def coda_paged_attention(Q, k_cache, v_cache, page_table, lengths, workspace, *, row_seq=None, scale=None, O=None,
+                         lse=None, scale_k=None, scale_v=None, stream=None):
+    """o = softmax(scale q K^T) V of one new token per row over its sequence's first ``lengths`` [M] int32 cached
+    keys.  Q [M, q_heads, head_dim], possibly a strided view of a QKV product's rows; caches, page_table and row_seq as
+    for coda_paged_append; ``scale`` defaults to 1 / sqrt(head_dim); ``lse`` [M, q_heads] fp32 is written when given.
+    Returns O [M, q_heads * head_dim]."""
+    lib = load_library()
+    if Q.dim() != 3:
+        raise ValueError(f"Q has {Q.dim()} dimensions, expected [M, q_heads, head_dim]")
+    M, q_heads, D = Q.shape
+    code = _dtype_code(Q)
+    pages, kv_heads, page_size, Dk, ccode = _cache_shape(k_cache, v_cache, Q.dtype)
+    if Dk != D:
+        raise ValueError(f"Q has head_dim {D}, the caches {Dk}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has {page_table.dim()} dimensions, expected [num_seqs, max_pages]")
+    _want(page_table, "page_table", dtypes=_I32)
+    _want(lengths, "lengths", (M,), _I32)
+    _want(row_seq, "row_seq", (M,), _I32)
+    _want(lse, "lse", (M, q_heads), _F32)
+    _want_scalars(scale_k=scale_k, scale_v=scale_v)
+    _want(workspace, "workspace", nbytes=lib.coda_paged_attention_workspace_bytes(q_heads, kv_heads, D))
+    if O is None:
+        O = torch.empty(M, q_heads * D, dtype=Q.dtype, device=Q.device)
+    _want(O, "O", (M, q_heads * D), (Q.dtype,))
+    q_ptr, ldq = _rows(Q, "Q")
+    _check(lib.coda_paged_attention(q_ptr, max(ldq, q_heads * D), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+                                    _dev(page_table, "page_table"), _dev(lengths, "lengths"),
+                                    _dev(row_seq, "row_seq"), _dev(O, "O"), _dev(lse, "lse"), M, page_table.shape[0],
+                                    page_table.shape[1], q_heads, kv_heads, D, pages, page_size,
+                                    D ** -0.5 if scale is None else float(scale), code, ccode,
+                                    _dev(scale_k, "scale_k"), _dev(scale_v, "scale_v"),
+                                    _dev(workspace, "workspace"), _stream(Q, stream)))
+    return O
+
+
+def _logits_rows(t, name):
+    """(pointer, row stride) of a logits matrix [M, V]; a single row's stride is rounded up to whole 16 bytes."""
+    ptr, ld = _rows(t, name)
+    if t.shape[0] <= 1:
+        step = 16 // t.element_size()
+        ld = -(-t.shape[1] // step) * step
+    return ptr, ld
+
+
+def coda_logprobs(logits, targets, top: int = 0, *, logp=None, entropy=None, lse=None, top_logp=None, top_ids=None,
+                  stream=None):
+    """Log probabilities of ``targets`` [M] int32 (negative: not scored) under softmax of ``logits`` [M, V] (rows may be
+    a strided view), with entropy, lse and the ``top`` best alternatives.  Returns a dict (logp, entropy, lse [M] fp32;
+    with top > 0 top_logp [M, top] fp32 and top_ids [M, top] int32)."""
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
+    M, V = logits.shape
+    _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
+    _want(targets, "targets", (M,), _I32)
+    e = lambda *shape, dt=torch.float32: torch.empty(*shape, dtype=dt, device=logits.device)  # noqa: E731
+    out = {"logp": e(M) if logp is None else logp, "entropy": e(M) if entropy is None else entropy,
+           "lse": e(M) if lse is None else lse}
+    if top > 0:
+        out["top_logp"] = e(M, top) if top_logp is None else top_logp
+        out["top_ids"] = e(M, top, dt=torch.int32) if top_ids is None else top_ids
+        _want(out["top_logp"], "top_logp", (M, top), _F32)
+        _want(out["top_ids"], "top_ids", (M, top), _I32)
+    for k in ("logp", "entropy", "lse"):
+        _want(out[k], k, (M,), _F32)
+    ptr, ld = _logits_rows(logits, "logits")
+    _check(lib.coda_logprobs(ptr, ld, _dev(targets, "targets"), _dev(out["logp"], "logp"),
+                             _dev(out["entropy"], "entropy"), _dev(out["lse"], "lse"),
+                             _dev(out.get("top_logp"), "top_logp"), _dev(out.get("top_ids"), "top_ids"), M, V, top,
+                             _dtype_code(logits), _stream(logits, stream)))
+    return out
+
+
+def coda_logprobs_backward(logits, targets, lse, entropy=None, dlogp=None, dentropy=None, dlogits=None, stream=None):
+    """dlogits = dlogp ([j = t] - p) - dentropy p (log p + entropy), from coda_logprobs' lse and entropy; dlogp and
+    dentropy [M] fp32 may be None (= 0).  ``dlogits`` [M, V] may be a strided view.  Returns dlogits."""
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
+    M, V = logits.shape
+    _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
+    _want(targets, "targets", (M,), _I32)
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        _want(t, name, (M,), _F32)
+    if dlogits is None:  # rows on 16-byte boundaries, as the logits' own
+        step = 16 // logits.element_size()
+        dlogits = torch.empty(M, -(-V // step) * step, dtype=logits.dtype, device=logits.device)[:, :V]
+    _want(dlogits, "dlogits", (M, V), (logits.dtype,))
+    ptr, ld = _logits_rows(logits, "logits")
+    dptr, ldd = _logits_rows(dlogits, "dlogits")
+    _check(lib.coda_logprobs_backward(ptr, ld, _dev(targets, "targets"), _dev(lse, "lse"), _dev(entropy, "entropy"),
+                                      _dev(dlogp, "dlogp"), _dev(dentropy, "dentropy"), dptr, ldd, M, V,
+                                      _dtype_code(logits), _stream(logits, stream)))
+    return dlogits
 
 
 def coda_amax(x, amax=None, stream=None):

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcoda_gb300.so")
 
-SOURCES = ["coda_gemm_bf16.cu", "coda_gemm_tf32.cu", "coda_gemm_e4m3.cu", "coda_aux.cu", "coda_abi.cu"]
+SOURCES = ["coda_gemm_bf16.cu", "coda_gemm_tf32.cu", "coda_gemm_e4m3.cu", "coda_aux.cu", "coda_paged.cu",
+           "coda_logprobs.cu", "coda_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -18,6 +18,13 @@ epilogue"; SwiGLU gate/up from the same section and "five blocks"):
   full_chain_train_forward / full_chain_backward, rowscale_block_backward
                   the training forward that saves G || U and r, and the
                   backward from that state (12 launches for the full chain)
+  decode_attention, decode_layer  one decode step of a layer around the block
+                  tail: the QKV rows into the paged cache (rotated on the way),
+                  attention over it, and full_chain on the result, whose Z is
+                  the next layer's QKV rows
+  head_logprobs / head_logprobs_backward  the LM head's GEMM on the last
+                  layer's h, log probabilities of given tokens, and their
+                  gradient down to h
 W' = diag(gamma) W is prepared once by ``fold_weights`` (coda_fold_gamma).
 The one-launch forms of the two blocks are the binding's coda_block_rowscale
 and coda_block_swiglu themselves.
@@ -224,3 +231,61 @@ def full_chain_backward(X, Wot, Wgut, Wdt, Wqt, gamma1, gamma2, fwd: dict, dZ, d
     return {"dX": coda_gemm(dh1, Wot, b_mn=True), "dR": dh1, "dWot": coda_gemm(dh1, X, a_mn=True, b_mn=True),
             "dWgut": dWgut, "dWdt": dWdt, "dWqt": dWqt, "dgamma1": dgamma1, "dgamma2": dgamma2, "dh2": dh2,
             "dGU": dGU}
+
+
+# ------------------------------------------------------ decode and scoring ----
+
+def decode_attention(Z, positions, lengths, page_table, k_cache, v_cache, q_heads: int, workspace, *, row_seq=None,
+                     base: float = 0.0, scale=None, scale_k=None, scale_v=None, bufs: Optional[dict] = None) -> dict:
+    """One new token per row: the QKV rows Z go into the paged cache at ``positions`` and each row attends to its
+    sequence's first ``lengths`` keys (2 launches).  ``base`` > 1 rotates Q and K on the way; 0 when Z's Q and K are
+    already rotated (coda_gemm_rowscale_rope), and then the queries are read out of Z itself.
+    ``workspace``: paged_attention_workspace(q_heads, kv_heads, head_dim)."""
+    from . import coda_paged_append, coda_paged_attention
+    D = k_cache.shape[3]
+    q = coda_paged_append(Z, positions, page_table, k_cache, v_cache, q_heads, row_seq=row_seq, base=base,
+                          Q=_b(bufs, "q") if base else None, want_q=bool(base), scale_k=scale_k, scale_v=scale_v)
+    if q is None:
+        q = Z[:, :q_heads * D].unflatten(1, (q_heads, D))
+    o = coda_paged_attention(q, k_cache, v_cache, page_table, lengths, workspace, row_seq=row_seq, scale=scale,
+                             O=_b(bufs, "o"), scale_k=scale_k, scale_v=scale_v)
+    return {"q": q, "o": o}
+
+
+def decode_layer(Z, R, positions, lengths, page_table, k_cache, v_cache, q_heads: int, workspace, Wot, Wgt_f, Wut_f,
+                 Wdt, Wqt_f, eps: float, *, row_seq=None, base: float = 0.0, scale=None, scale_k=None, scale_v=None,
+                 bufs: Optional[dict] = None) -> dict:
+    """decode_attention and full_chain on its output: R is the residual stream the QKV rows Z were projected from.
+    Returns full_chain's outputs (h2 is the next residual stream, Z the next layer's QKV rows, or the LM head's
+    logits when Wqt_f is its weight) and q, o."""
+    a = decode_attention(Z, positions, lengths, page_table, k_cache, v_cache, q_heads, workspace, row_seq=row_seq,
+                         base=base, scale=scale, scale_k=scale_k, scale_v=scale_v, bufs=bufs)
+    return {**full_chain(a["o"], Wot, R, Wgt_f, Wut_f, Wdt, Wqt_f, eps, bufs, fused_reduce=True), **a}
+
+
+def head_logprobs(h, P, Wvt_f, eps: float, targets, top: int = 0, vocab: Optional[int] = None,
+                  bufs: Optional[dict] = None) -> dict:
+    """The LM head on the residual stream h and its partials P (as coda_gemm_residual_partial_rms wrote them):
+    logits = RMSNorm(h) Wv, then log probabilities of ``targets`` with entropy, lse and the ``top`` best alternatives.
+    ``vocab``: the number of tokens when Wvt_f has padded rows behind them.  Returns coda_logprobs' dict and logits, r."""
+    from . import coda_logprobs
+    logits, r = _rowscale(h, Wvt_f, P, eps, bufs, "r", "logits", True)
+    got = coda_logprobs(logits if vocab is None else logits[:, :vocab], targets, top,
+                        **{k: _b(bufs, k) for k in ("logp", "entropy", "lse", "top_logp", "top_ids")})
+    return {**got, "logits": logits, "r": r}
+
+
+def head_logprobs_backward(h, Wvt, gamma, fwd: dict, targets, dlogp=None, dentropy=None,
+                           vocab: Optional[int] = None) -> dict:
+    """Gradients of head_logprobs (bf16): dh, dWvt and dgamma from the upstream dlogp and dentropy.  Wvt is the unfolded
+    head weight, ``fwd`` what head_logprobs returned."""
+    from . import coda_gemm, coda_gemm_grad_norm, coda_logprobs_backward, coda_rmsnorm_backward
+    logits = fwd["logits"]
+    V = logits.shape[1] if vocab is None else vocab
+    # the padded tokens' columns take part in no softmax: their gradient is 0
+    dlogits = torch.empty_like(logits) if V == logits.shape[1] else torch.zeros_like(logits)
+    coda_logprobs_backward(logits[:, :V], targets, fwd["lse"], fwd["entropy"], dlogp, dentropy, dlogits[:, :V])
+    dy, S = coda_gemm_grad_norm(dlogits, Wvt, h, gamma)
+    dh, Yt, dgamma = coda_rmsnorm_backward(dy, h, fwd["r"], gamma, S)
+    return {"dlogits": dlogits, "dh": dh, "dgamma": dgamma,
+            "dWvt": coda_gemm(dlogits, Yt, a_mn=True, b_mn=True, col_scale=gamma)}

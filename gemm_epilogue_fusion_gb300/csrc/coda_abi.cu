@@ -1036,10 +1036,282 @@ coda_status coda_get_device_status(void) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   const unsigned s = coda::read_clear_status_bf16() | coda::read_clear_status_tf32() |
-                     coda::read_clear_status_e4m3() | coda::read_clear_status_aux();
+                     coda::read_clear_status_e4m3() | coda::read_clear_status_aux() |
+                     coda::read_clear_status_paged() | coda::read_clear_status_logprobs();
   if (s == ~0u) return fail(CODA_ERR_CUDA, "could not read the device status word");
   if (s & 1u) return fail(CODA_ERR_TIMEOUT, "a kernel gave up on a bounded wait (timeout)");
+  if (s & 2u)
+    return fail(CODA_ERR_INVALID_ARG, "a page, sequence, length or token index on the device was out of range");
   return CODA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- paged cache, attention ----
+namespace {
+
+// Shape rules common to the paged cache calls.
+coda_status check_paged(int64_t M, int64_t num_seqs, int64_t max_pages, int64_t q_heads, int64_t kv_heads,
+                        int64_t head_dim, int64_t num_pages, int64_t page_size, const int32_t* row_seq,
+                        coda_dtype dtype, coda_dtype cache_dtype, const float* scale_k, const float* scale_v) {
+  REQUIRE(dtype == CODA_F32 || dtype == CODA_BF16, "dtype must be CODA_F32 or CODA_BF16");
+  REQUIRE(cache_dtype == dtype || (dtype == CODA_BF16 && cache_dtype == CODA_E4M3),
+          "cache_dtype must equal dtype, or be CODA_E4M3 with CODA_BF16");
+  REQUIRE(M >= 0 && M < INT32_MAX, "M = %" PRId64 " out of range [0, 2^31)", M);
+  REQUIRE(num_seqs >= 0 && num_seqs < INT32_MAX, "num_seqs = %" PRId64 " out of range [0, 2^31)", num_seqs);
+  REQUIRE(row_seq != nullptr || M <= num_seqs, "M = %" PRId64 " rows but %" PRId64 " sequences, and row_seq is NULL", M,
+          num_seqs);
+  REQUIRE(max_pages > 0 && max_pages < INT32_MAX, "max_pages = %" PRId64 " out of range [1, 2^31)", max_pages);
+  REQUIRE(num_pages > 0 && num_pages < INT32_MAX, "num_pages = %" PRId64 " out of range [1, 2^31)", num_pages);
+  REQUIRE(page_size > 0 && page_size < INT32_MAX, "page_size = %" PRId64 " out of range [1, 2^31)", page_size);
+  REQUIRE(kv_heads > 0 && q_heads > 0 && q_heads < (1 << 20) && q_heads % kv_heads == 0,
+          "q_heads = %" PRId64 " must be a positive multiple of kv_heads = %" PRId64 ", below 2^20", q_heads, kv_heads);
+  const int64_t step = 16 / elem_bytes(cache_dtype);
+  REQUIRE(head_dim > 0 && head_dim <= coda::kMaxHeadDim && head_dim % step == 0,
+          "head_dim = %" PRId64 " must be a multiple of %" PRId64 " for this cache, at most %d", head_dim, step,
+          coda::kMaxHeadDim);
+  REQUIRE(num_pages < (int64_t(1) << 60) / page_size / kv_heads / head_dim, "a cache of 2^60 elements or more");
+  REQUIRE(M < (int64_t(1) << 60) / (q_heads + 2 * kv_heads) / head_dim, "rows of 2^60 elements or more");
+  REQUIRE(num_seqs * max_pages < (int64_t(1) << 60), "a page table of 2^60 entries or more");
+  if (cache_dtype == CODA_E4M3) {
+    TRY(check_scalar_ptr(scale_k, "scale_k"));
+    TRY(check_scalar_ptr(scale_v, "scale_v"));
+  } else {
+    REQUIRE(scale_k == nullptr && scale_v == nullptr, "scale_k and scale_v must be NULL unless the cache is CODA_E4M3");
+  }
+  return CODA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+coda_status coda_paged_append(const void* Z, const int32_t* positions, const int32_t* row_seq,
+                              const int32_t* page_table, void* Q, void* Kc, void* Vc, int64_t M, int64_t num_seqs,
+                              int64_t max_pages, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t num_pages, int64_t page_size, double base, coda_dtype dtype,
+                              coda_dtype cache_dtype, const float* scale_k, const float* scale_v,
+                              cudaStream_t stream) {
+  g_msg[0] = 0;
+  TRY(check_paged(M, num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size, row_seq, dtype,
+                  cache_dtype, scale_k, scale_v));
+  REQUIRE(base == 0.0 || (std::isfinite(base) && base > 1.0), "base must be 0 (no rotation), or finite and > 1");
+  if (M == 0) return CODA_OK;
+  TRY(check_ptr(Z, "Z"));
+  TRY(check_scalar_ptr(positions, "positions"));
+  if (row_seq) TRY(check_scalar_ptr(row_seq, "row_seq"));
+  TRY(check_scalar_ptr(page_table, "page_table"));
+  if (Q) TRY(check_ptr(Q, "Q"));
+  TRY(check_ptr(Kc, "k_cache"));
+  TRY(check_ptr(Vc, "v_cache"));
+  const int64_t eb = elem_bytes(dtype), cache = num_pages * page_size * kv_heads * head_dim * elem_bytes(cache_dtype);
+  const Range outs[] = {rng("Q", Q, Q ? M * q_heads * head_dim * eb : 0), rng("k_cache", Kc, cache),
+                        rng("v_cache", Vc, cache)};
+  const Range ins[] = {rng("Z", Z, M * (q_heads + 2 * kv_heads) * head_dim * eb),
+                       rng("positions", positions, M * 4),
+                       rng("row_seq", row_seq, row_seq ? M * 4 : 0),
+                       rng("page_table", page_table, num_seqs * max_pages * 4),
+                       rng("scale_k", scale_k, scale_k ? 4 : 0),
+                       rng("scale_v", scale_v, scale_v ? 4 : 0)};
+  TRY(check_overlaps(outs, 3, ins, 6));
+  coda::AppendParams p = {};
+  p.Z = Z;
+  p.positions = positions;
+  p.row_seq = row_seq;
+  p.page_table = page_table;
+  p.Q = Q;
+  p.Kc = Kc;
+  p.Vc = Vc;
+  p.scale_k = scale_k;
+  p.scale_v = scale_v;
+  p.num_seqs = static_cast<int>(num_seqs);
+  p.max_pages = static_cast<int>(max_pages);
+  p.q_heads = static_cast<int>(q_heads);
+  p.kv_heads = static_cast<int>(kv_heads);
+  p.head_dim = static_cast<int>(head_dim);
+  p.num_pages = static_cast<int>(num_pages);
+  p.page_size = static_cast<int>(page_size);
+  p.rotate = base != 0.0;
+  if (p.rotate) {
+    // base^(-2j / head_dim) / 2 pi < 1 as a 64-bit fraction of a turn, by repeated products in 64 bits: the
+    // relative error of term j is j 2^-53, so the turn count at position 2^31 is off by less than 1e-6 of a turn
+    const double ratio = std::pow(base, -2.0 / static_cast<double>(head_dim));
+    double f = 0.15915494309189535 * 0x1p64;
+    for (int64_t j = 0; j < head_dim / 2; ++j, f *= ratio) p.turn[j] = static_cast<uint64_t>(f);
+  }
+  cudaError_t e =
+      coda::launch_paged_append(p, M, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
+  return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_paged_append launch");
+}
+
+int64_t coda_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  if (kv_heads <= 0 || q_heads <= 0 || q_heads >= (1 << 20) || q_heads % kv_heads != 0 || head_dim <= 0 ||
+      head_dim > coda::kMaxHeadDim)
+    return -1;
+  return coda::paged_attention_workspace_bytes(static_cast<int>(q_heads), static_cast<int>(kv_heads),
+                                               static_cast<int>(head_dim));
+}
+
+coda_status coda_paged_attention(const void* Q, int64_t ldq, const void* Kc, const void* Vc,
+                                 const int32_t* page_table, const int32_t* lengths, const int32_t* row_seq, void* O,
+                                 float* lse, int64_t M, int64_t num_seqs, int64_t max_pages, int64_t q_heads,
+                                 int64_t kv_heads, int64_t head_dim, int64_t num_pages, int64_t page_size,
+                                 float scale, coda_dtype dtype, coda_dtype cache_dtype, const float* scale_k,
+                                 const float* scale_v, void* workspace, cudaStream_t stream) {
+  g_msg[0] = 0;
+  TRY(check_paged(M, num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size, row_seq, dtype,
+                  cache_dtype, scale_k, scale_v));
+  const int64_t eb = elem_bytes(dtype), width = q_heads * head_dim;
+  REQUIRE(ldq >= width && ldq < (int64_t(1) << 40) && (ldq * eb) % 16 == 0,
+          "ldq = %" PRId64 " must hold a row of %" PRId64 " elements and be a multiple of %" PRId64, ldq, width, 16 / eb);
+  REQUIRE(std::isfinite(scale) && scale > 0.0f, "scale must be finite and > 0");
+  REQUIRE(M * q_heads < INT32_MAX, "M * q_heads = %" PRId64 " out of range [0, 2^31)", M * q_heads);
+  REQUIRE(M == 0 || ldq < (int64_t(1) << 60) / M, "rows of 2^60 elements or more");
+  if (M == 0) return CODA_OK;
+  TRY(check_ptr(Q, "Q"));
+  TRY(check_ptr(Kc, "k_cache"));
+  TRY(check_ptr(Vc, "v_cache"));
+  TRY(check_scalar_ptr(page_table, "page_table"));
+  TRY(check_scalar_ptr(lengths, "lengths"));
+  if (row_seq) TRY(check_scalar_ptr(row_seq, "row_seq"));
+  TRY(check_ptr(O, "O"));
+  if (lse) TRY(check_scalar_ptr(lse, "lse"));
+  TRY(check_ptr(workspace, "workspace"));
+  const int64_t cache = num_pages * page_size * kv_heads * head_dim * elem_bytes(cache_dtype);
+  const Range outs[] = {rng("O", O, M * width * eb), rng("lse", lse, lse ? M * q_heads * 4 : 0),
+                        rng("workspace", workspace, coda_paged_attention_workspace_bytes(q_heads, kv_heads, head_dim))};
+  const Range ins[] = {rng("Q", Q, ((M - 1) * ldq + width) * eb),
+                       rng("k_cache", Kc, cache),
+                       rng("v_cache", Vc, cache),
+                       rng("page_table", page_table, num_seqs * max_pages * 4),
+                       rng("lengths", lengths, M * 4),
+                       rng("row_seq", row_seq, row_seq ? M * 4 : 0),
+                       rng("scale_k", scale_k, scale_k ? 4 : 0),
+                       rng("scale_v", scale_v, scale_v ? 4 : 0)};
+  TRY(check_overlaps(outs, 3, ins, 8));
+  coda::AttnParams p = {};
+  p.Q = Q;
+  p.ldq = ldq;
+  p.Kc = Kc;
+  p.Vc = Vc;
+  p.page_table = page_table;
+  p.lengths = lengths;
+  p.row_seq = row_seq;
+  p.O = O;
+  p.lse = lse;
+  p.scale_k = scale_k;
+  p.scale_v = scale_v;
+  p.workspace = workspace;
+  p.scale = scale;
+  p.M = static_cast<int>(M);
+  p.num_seqs = static_cast<int>(num_seqs);
+  p.max_pages = static_cast<int>(max_pages);
+  p.q_heads = static_cast<int>(q_heads);
+  p.kv_heads = static_cast<int>(kv_heads);
+  p.head_dim = static_cast<int>(head_dim);
+  p.num_pages = static_cast<int>(num_pages);
+  p.page_size = static_cast<int>(page_size);
+  cudaError_t e = coda::launch_paged_attention(p, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
+  return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_paged_attention launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- log probabilities ----
+namespace {
+
+// Shape rules common to the log-probability calls.
+coda_status check_logits(int64_t M, int64_t V, int64_t ld, const char* ldname, coda_dtype dtype) {
+  REQUIRE(dtype == CODA_F32 || dtype == CODA_BF16, "dtype must be CODA_F32 or CODA_BF16");
+  REQUIRE(M >= 0 && M < INT32_MAX, "M = %" PRId64 " out of range [0, 2^31)", M);
+  REQUIRE(V > 0 && V < INT32_MAX / 2, "V = %" PRId64 " out of range [1, 2^30)", V);
+  REQUIRE(ld >= V && ld < (int64_t(1) << 40) && (ld * elem_bytes(dtype)) % 16 == 0,
+          "%s = %" PRId64 " must be at least V = %" PRId64 " and a multiple of %d", ldname, ld, V,
+          16 / elem_bytes(dtype));
+  REQUIRE(M == 0 || ld < (int64_t(1) << 60) / M, "rows of 2^60 elements or more");
+  return CODA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+coda_status coda_logprobs(const void* logits, int64_t ld, const int32_t* targets, float* logp, float* entropy,
+                          float* lse, float* top_logp, int32_t* top_ids, int64_t M, int64_t V, int64_t top,
+                          coda_dtype dtype, cudaStream_t stream) {
+  g_msg[0] = 0;
+  TRY(check_logits(M, V, ld, "ld", dtype));
+  REQUIRE(top >= 0 && top <= coda::kMaxTop && top <= V, "top = %" PRId64 " out of range [0, min(V, %d)]", top,
+          coda::kMaxTop);
+  if (M == 0) return CODA_OK;
+  TRY(check_ptr(logits, "logits"));
+  TRY(check_scalar_ptr(targets, "targets"));
+  TRY(check_scalar_ptr(logp, "logp"));
+  if (entropy) TRY(check_scalar_ptr(entropy, "entropy"));
+  if (lse) TRY(check_scalar_ptr(lse, "lse"));
+  if (top > 0) {
+    TRY(check_scalar_ptr(top_logp, "top_logp"));
+    TRY(check_scalar_ptr(top_ids, "top_ids"));
+  }
+  const Range outs[] = {rng("logp", logp, M * 4), rng("entropy", entropy, entropy ? M * 4 : 0),
+                        rng("lse", lse, lse ? M * 4 : 0), rng("top_logp", top_logp, M * top * 4),
+                        rng("top_ids", top_ids, M * top * 4)};
+  const Range ins[] = {rng("logits", logits, ((M - 1) * ld + V) * elem_bytes(dtype)),
+                       rng("targets", targets, M * 4)};
+  TRY(check_overlaps(outs, 5, ins, 2));
+  coda::LogprobsParams p = {};
+  p.logits = logits;
+  p.ld = ld;
+  p.targets = targets;
+  p.logp = logp;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.top_logp = top_logp;
+  p.top_ids = top_ids;
+  p.V = static_cast<int>(V);
+  p.top = static_cast<int>(top);
+  cudaError_t e = coda::launch_logprobs(p, M, dtype == CODA_F32, stream, use_pdl());
+  return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_logprobs launch");
+}
+
+coda_status coda_logprobs_backward(const void* logits, int64_t ld, const int32_t* targets, const float* lse,
+                                   const float* entropy, const float* dlogp, const float* dentropy, void* dlogits,
+                                   int64_t ldd, int64_t M, int64_t V, coda_dtype dtype, cudaStream_t stream) {
+  g_msg[0] = 0;
+  TRY(check_logits(M, V, ld, "ld", dtype));
+  TRY(check_logits(M, V, ldd, "ldd", dtype));
+  if (M == 0) return CODA_OK;
+  TRY(check_ptr(logits, "logits"));
+  TRY(check_scalar_ptr(targets, "targets"));
+  TRY(check_scalar_ptr(lse, "lse"));
+  if (dlogp) TRY(check_scalar_ptr(dlogp, "dlogp"));
+  if (dentropy) {
+    TRY(check_scalar_ptr(dentropy, "dentropy"));
+    TRY(check_scalar_ptr(entropy, "entropy"));
+  }
+  TRY(check_ptr(dlogits, "dlogits"));
+  const int eb = elem_bytes(dtype);
+  const Range outs[] = {rng("dlogits", dlogits, ((M - 1) * ldd + V) * eb)};
+  const Range ins[] = {rng("logits", logits, ((M - 1) * ld + V) * eb),
+                       rng("targets", targets, M * 4),
+                       rng("lse", lse, M * 4),
+                       rng("entropy", entropy, entropy ? M * 4 : 0),
+                       rng("dlogp", dlogp, dlogp ? M * 4 : 0),
+                       rng("dentropy", dentropy, dentropy ? M * 4 : 0)};
+  TRY(check_overlaps(outs, 1, ins, 6));
+  coda::LogprobsGradParams p = {};
+  p.logits = logits;
+  p.ld = ld;
+  p.targets = targets;
+  p.lse = lse;
+  p.entropy = dentropy ? entropy : nullptr;
+  p.dlogp = dlogp;
+  p.dentropy = dentropy;
+  p.dlogits = dlogits;
+  p.ldd = ldd;
+  p.V = static_cast<int>(V);
+  cudaError_t e = coda::launch_logprobs_backward(p, M, dtype == CODA_F32, stream, use_pdl());
+  return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_logprobs_backward launch");
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ namespace coda {
 // Device status bits, OR-ed into the status word of the kernel's translation
 // unit and read back (and cleared) by coda_get_device_status().
 constexpr unsigned kDevTimeout = 1u;
+constexpr unsigned kDevBadIndex = 2u;  // a page, sequence or token index read on the device was out of range
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -34,6 +34,10 @@
  * either operand layout, coda_gemm_swiglu_save / coda_gemm_swiglu_backward),
  * quantise to FP8 (coda_amax, coda_quantize_e4m3), and run an FP8 block in
  * one launch that quantises its own operands (coda_block_*_fp8).
+ * Around the block, a decode step appends the QKV product to a paged cache
+ * (coda_paged_append) and attends to it (coda_paged_attention), and the LM
+ * head's logits give log probabilities and their gradient (coda_logprobs,
+ * coda_logprobs_backward).
  *
  * Conventions shared by every call
  *   - Matrices are row-major.  Activations are [rows, K]; a weight W [K, N]
@@ -409,6 +413,123 @@ CODA_API coda_status coda_gemm_swiglu_backward(const void* dOut, const void* Wt,
                                                int64_t M, int64_t I, int64_t K, coda_dtype dtype,
                                                cudaStream_t stream);
 
+/* ---- Decode and scoring: what runs between the QKV projection and the next
+ * block tail when a model answers token by token, and on the logits of its LM
+ * head (the row-scale GEMM with the head's weight).  Not on the pages: they
+ * describe the block's GEMMs; these calls are the rest of a decode step.
+ *
+ * The paged cache.  Keys and values live in two caches of the same shape
+ * [num_pages, kv_heads, page_size, head_dim]; position t of sequence b is slot
+ * t mod page_size of page page_table[b, t / page_size] (page_table
+ * [num_seqs, max_pages] int32; only the entries that a row needs are read).
+ *   dtype CODA_F32 with a CODA_F32 cache, or CODA_BF16 with a CODA_BF16 or a
+ *   CODA_E4M3 cache.  An e4m3 cache has per-tensor scales (device fp32
+ *   scalars scale_k, scale_v; NULL otherwise): a code c stands for c * scale,
+ *   and a value x is stored as e4m3(x / scale), rounded and saturated as by
+ *   coda_quantize_e4m3.
+ *   head_dim: at most 256, a multiple of 4 (fp32), 8 (bf16) or 16 (e4m3
+ *   cache).  q_heads: a multiple of kv_heads; query head h reads key/value
+ *   head h / (q_heads / kv_heads).  page_size, num_pages >= 1.
+ *   row_seq [M] int32: the sequence of each row, or NULL when row i belongs
+ *   to sequence i (M <= num_seqs then).  Several rows may belong to one
+ *   sequence.
+ *   Index values are on the device, so the kernels check them: a row whose
+ *   sequence, position or page is out of range raises the device status
+ *   (CODA_ERR_INVALID_ARG from coda_get_device_status()) and is left out as
+ *   described below; nothing out of bounds is read or written.
+ */
+
+/* Appends M rows of a QKV product to the paged cache, with the position
+ * rotation of coda_gemm_rowscale_rope (interleaved pairs) applied on the way:
+ *   Z         [M, (q_heads + 2 kv_heads) * head_dim], dtype: query heads, key
+ *             heads, value heads
+ *   positions [M] int32: the position p of each row.  p < 0: a padded row,
+ *             nothing of it is read or written.
+ *   base      0: Z's heads are taken as they are (already rotated by the
+ *             GEMM's epilogue); else finite, > 1: pair j of every query and
+ *             key head turns by p * base^(-2j / head_dim).  The angle is kept
+ *             as a 64-bit fraction of a turn, so it does not lose precision
+ *             at far positions.
+ *   Q         [M, q_heads * head_dim], dtype: the rotated queries; nullable
+ *             (then only the caches are written)
+ *   k_cache, v_cache: written at the rows' slots only.
+ * Values are computed in fp32 and rounded once to the type they are stored in.
+ * A row with an index out of range is left out whole (its Q row as well).
+ * Two rows of one call must not name the same slot (the slot would hold a
+ * mixture of the two); a page may be shared by sequences that only read it. */
+CODA_API coda_status coda_paged_append(const void* Z, const int32_t* positions, const int32_t* row_seq,
+                                       const int32_t* page_table, void* Q, void* k_cache, void* v_cache, int64_t M,
+                                       int64_t num_seqs, int64_t max_pages, int64_t q_heads, int64_t kv_heads,
+                                       int64_t head_dim, int64_t num_pages, int64_t page_size, double base,
+                                       coda_dtype dtype, coda_dtype cache_dtype, const float* scale_k,
+                                       const float* scale_v, cudaStream_t stream);
+
+/* Attention of one new token per row over the paged cache:
+ *   s_t = scale * q . k_t for t in [0, lengths[i]),  o = sum_t softmax(s)_t v_t
+ *   Q       rows of [q_heads, head_dim] elements (dtype), ldq elements apart
+ *           (ldq = q_heads * head_dim, or the row stride of a QKV product
+ *           whose leading columns are the queries)
+ *   lengths [M] int32: keys of the row, its own included when it has been
+ *           appended.  <= 0: no keys.
+ *   scale   finite, > 0 (1 / sqrt(head_dim) as a rule)
+ *   O       [M, q_heads * head_dim], dtype
+ *   lse     nullable [M, q_heads] fp32: log sum_t exp(s_t)
+ * Scores, the running maximum and sum, and the outputs are held in fp32.
+ * A row without keys, or whose scores are all -inf, gives o = 0 and lse =
+ * -inf.  Slots behind lengths[i] are never read into the result, whatever
+ * they hold; NaN in a key or value of the row itself propagates.  M * q_heads < 2^31.
+ * A row whose sequence is out of range counts as a row without keys, a length
+ * beyond max_pages * page_size as that length, and keys on a page out of
+ * range are left out; each raises the device status.
+ * The same inputs give the same bits on every call on one device.
+ * workspace: coda_paged_attention_workspace_bytes(q_heads, kv_heads,
+ *   head_dim) bytes of device memory (the same for any M and lengths; -1 for
+ *   heads out of range), zeroed by the caller before its first use; every call
+ *   leaves it ready for the next.  Calls (or captured graphs) that share a
+ *   workspace must not overlap on the GPU. */
+CODA_API int64_t coda_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+CODA_API coda_status coda_paged_attention(const void* Q, int64_t ldq, const void* k_cache, const void* v_cache,
+                                          const int32_t* page_table, const int32_t* lengths, const int32_t* row_seq,
+                                          void* O, float* lse, int64_t M, int64_t num_seqs, int64_t max_pages,
+                                          int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t num_pages,
+                                          int64_t page_size, float scale, coda_dtype dtype, coda_dtype cache_dtype,
+                                          const float* scale_k, const float* scale_v, void* workspace,
+                                          cudaStream_t stream);
+
+/* Log probabilities of given tokens under softmax of logits x, with entropy
+ * and the best alternatives:
+ *   lse = log sum_j exp x_j,  logp = x_t - lse,  entropy = -sum_j p_j log p_j
+ *   logits   rows of V elements (CODA_F32 or CODA_BF16), ld elements apart;
+ *            ld gives 16-byte rows, V is any width in [1, 2^30)
+ *   targets  [M] int32: the token t of each row.  t < 0: not scored, logp = 0.
+ *            t >= V: the same, and the device status is raised.
+ *   logp     [M] fp32;  entropy, lse: nullable [M] fp32
+ *   top      number of alternatives, 0 to min(V, 64):
+ *   top_logp [M, top] fp32 and top_ids [M, top] int32: the largest log
+ *            probabilities in falling order, ties by the lower index (NULL
+ *            when top = 0).
+ * Statistics are held in fp32.  -inf logits have probability 0; a row of
+ * nothing but -inf gives lse = logp = top_logp = -inf and entropy 0.  A row
+ * that holds NaN or +inf gives NaN statistics (alternatives: NaN first, then
+ * by value). */
+CODA_API coda_status coda_logprobs(const void* logits, int64_t ld, const int32_t* targets, float* logp,
+                                   float* entropy, float* lse, float* top_logp, int32_t* top_ids, int64_t M,
+                                   int64_t V, int64_t top, coda_dtype dtype, cudaStream_t stream);
+
+/* Gradient of coda_logprobs' logp and entropy with respect to the logits:
+ *   dlogits_j = dlogp ([j = t] - p_j) - dentropy p_j (x_j - lse + entropy)
+ *   lse, entropy: as coda_logprobs wrote them (entropy may be NULL without
+ *            dentropy)
+ *   dlogp, dentropy: nullable [M] fp32 upstream gradients (NULL = 0)
+ *   dlogits  rows of V elements in the logits' type, ldd elements apart; the
+ *            columns [V, ldd) are left as they are.  May not overlap logits.
+ * A row that is not scored (t < 0 or t >= V) has dlogp = 0; a row of nothing
+ * but -inf (lse = -inf) has gradient 0.  The alternatives carry no gradient. */
+CODA_API coda_status coda_logprobs_backward(const void* logits, int64_t ld, const int32_t* targets, const float* lse,
+                                            const float* entropy, const float* dlogp, const float* dentropy,
+                                            void* dlogits, int64_t ldd, int64_t M, int64_t V, coda_dtype dtype,
+                                            cudaStream_t stream);
+
 /* Per-tensor absolute maximum: *amax = max_i |x_i| over n elements of
  * dtype CODA_F32 or CODA_BF16 (overwritten).  n may be 0 (amax = 0).
  * The FP8 operands of the block's LLaMA-8B workload use per-tensor scales. */
@@ -437,7 +558,9 @@ CODA_API coda_status coda_selftest_wait_timeout(int64_t timeout_ns, cudaStream_t
 
 /* Synchronises the current device, then reads and clears the device status
  * word: CODA_ERR_TIMEOUT if any kernel since the last call gave up on a
- * bounded wait, CODA_ERR_CUDA if the device reports an error, else CODA_OK. */
+ * bounded wait, CODA_ERR_INVALID_ARG if one met an index out of range in
+ * device memory (the paged cache and log-probability calls), CODA_ERR_CUDA if
+ * the device reports an error, else CODA_OK. */
 CODA_API coda_status coda_get_device_status(void);
 
 #ifdef __cplusplus
