@@ -5,9 +5,11 @@
 // Cache layout: [num_pages, kv_heads, page_size, head_dim], so that a page's
 // rows of one head are contiguous.  Nothing here waits on another block.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -24,7 +26,6 @@ __device__ unsigned g_paged_status;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__nv_fp8_e4m3 x) { return static_cast<float>(x); }
 template <class T>
 __device__ __forceinline__ T from_f32(float x);
 template <>
@@ -83,111 +84,794 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
   }
 }
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnGroup = 8;  // query heads per block
 
-// One block per row, key/value head and group of up to 8 of its query heads.
-// Each warp takes every fourth key with its own running maximum and sum; the
-// warps are joined at the end.
-template <class T, class C>
-__global__ void __launch_bounds__(32 * kAttnWarps) attention_kernel(const __grid_constant__ AttnParams p) {
+// ---------------------------------------------------------------- attention ----
+// One new token per row, flash-decoding style: o = sum_t p_t v_t / sum_t p_t,
+// p_t = 2^(s_t - m), with the running maximum m, the sum and o kept in fp32 and
+// every key and value read once.
+//
+// What bounds it: a key of G query heads is 4 G D operations on 2 D e bytes, so
+// for any G up to 16 the bytes of the cache decide.  Everything serves the loads:
+//   - the work is cut into tiles of kAttnWarps * KT keys of one row and key/value
+//     head, and each block of a grid that fills the GPU takes an equal run of
+//     consecutive tiles, whatever the rows' lengths (the lengths are on the
+//     device: every block computes the same partition from them);
+//   - each warp has its own keys of a tile, its own ring of ST stages filled with
+//     cp.async and its own running m, sum and o: no barrier in the loop.  Page
+//     numbers are read a tile ahead of the loads that need them;
+//   - a row and head whose tiles lie in one block is finished there; otherwise
+//     each block leaves (m, sum, o) in the workspace and the block that comes
+//     last joins them in the order of the keys, so the bits do not depend on
+//     which one it was.  No block waits for another.
+// The products run on mma.sync with the query heads as the 16 rows of the
+// instruction (tcgen05's smallest tile has 64, and its operands would have to
+// be rearranged in shared memory page by page): at the full HBM rate they need
+// about a fifth of the tensor pipe.  fp32 runs on the FMA pipe.
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kMaxWorkers = 512;  // blocks of a grid: bounds the workspace
+constexpr int kMinTiles = 2;      // tiles a block takes at least
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <class T, class C, int DP_, bool WIDE_>
+struct AttnShape {
+  static constexpr bool F32 = sizeof(T) == 4;
+  static constexpr bool E4M3 = sizeof(C) == 1;
+  static constexpr bool WIDE = WIDE_;  // more than 8 (fp32: more than 1) query heads of a key/value head at a time
+  static constexpr int DP = DP_;       // head_dim rounded up
+  static constexpr int RG = F32 ? (WIDE ? 8 : 1) : (WIDE ? 16 : 8);  // query heads of a block
+  static constexpr int PITCH = DP * static_cast<int>(sizeof(C));     // bytes of a staged row
+  static constexpr int KT0 = 4096 / PITCH, KMIN = F32 ? 8 : 16;
+  static constexpr int KT = F32 ? (DP == 256 ? 8 : 16) : (KT0 < KMIN ? KMIN : KT0);  // keys of a warp's tile
+  static constexpr int CT = KT * kAttnWarps;
+  static constexpr int ST = 3;
+  static constexpr int KPL = (KT + 31) / 32;  // keys per lane when pages are looked up
+  static constexpr int STAGE = 2 * KT * PITCH;
+  static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
+  static constexpr int RING = kAttnWarps * ST * STAGE;
+  static constexpr int JOIN = 2 * RG * DP * 4;
+  static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : 0;
+  static constexpr int SMEM = RING + JOIN + QBYTES;
+  static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;
+};
+
+// Chunk c of staged row `row`: 16-byte chunks are permuted within 128 bytes so
+// that eight rows' equal chunks lie in different banks.
+template <int PITCH>
+__device__ __forceinline__ int staged(int row, int c) {
+  constexpr int GROUP = PITCH >= 128 ? 8 : PITCH / 16, STEP = PITCH >= 128 ? 1 : 128 / PITCH;
+  return row * PITCH + ((c ^ ((row / STEP) & (GROUP - 1))) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// c [16 x 8] += a [16 x 16] b [16 x 8], f16 or bf16 operands, fp32 sums.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (the low 16 bits) as f16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(codes));
+  return d;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  if constexpr (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// What the kernel knows of a row: keys that count, and its sequence.
+struct RowInfo {
+  int len, seq;
+};
+__device__ __forceinline__ RowInfo row_info(const AttnParams& p, int row, bool& bad) {
+  RowInfo r;
+  r.len = max(p.lengths[row], 0);
+  r.seq = p.row_seq ? p.row_seq[row] : row;
+  const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+  if (r.len > room) {
+    r.len = static_cast<int>(room);
+    bad = true;
+  }
+  if (r.len > 0 && (r.seq < 0 || r.seq >= p.num_seqs)) {
+    r.len = 0;
+    bad = true;
+  }
+  return r;
+}
+
+// A tile in a block's run: tile t of nt of row `row` and head unit h (a
+// key/value head and a group of its query heads).
+struct Cursor {
+  int row, h, t, nt, len, seq;
+  __device__ __forceinline__ void enter(const AttnParams& p, int CT) {
+    bool bad = false;
+    const RowInfo r = row_info(p, row, bad);
+    len = r.len;
+    seq = r.seq;
+    nt = max(1, (len + CT - 1) / CT);
+  }
+  __device__ __forceinline__ void next(const AttnParams& p, int units, int CT) {
+    if (++t < nt) return;
+    t = 0;
+    if (++h < units) return;
+    h = 0;
+    if (++row < p.M) enter(p, CT);
+  }
+};
+
+template <class E, class C, int DP, bool WIDE>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
+    attention_kernel(const __grid_constant__ AttnParams p) {
+  using S = AttnShape<E, C, DP, WIDE>;
+  constexpr int KT = S::KT, CT = S::CT, ST = S::ST, PITCH = S::PITCH, CPR = S::CPR, KPL = S::KPL, RG = S::RG;
+  constexpr bool F16 = S::E4M3;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scan[kAttnWarps];
+  __shared__ int s_start[3], s_last;
+  __shared__ uint32_t s_mask[kAttnWarps][ST][2];
+  __shared__ float s_ml[2][RG][2];
+  float* s_o = reinterpret_cast<float*>(smem + S::RING);  // [2][RG][DP]
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int G = p.q_heads / p.kv_heads, groups = (G + RG - 1) / RG, gsize = (G + groups - 1) / groups;
+  const int units = p.kv_heads * groups;
+  const int chunks = p.head_dim * static_cast<int>(sizeof(C)) / 16;
+  const uint32_t ring = smem_u32(smem) + w * ST * S::STAGE;
+
+  // columns [head_dim, DP) of the ring are never loaded: zero once
+  if (chunks < CPR)
+    for (int i = tid; i < S::RING / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int NE = 8;  // head_dim <= 256
-  __shared__ float s_m[kAttnWarps][kAttnGroup], s_l[kAttnWarps][kAttnGroup];
-  __shared__ float s_o[kAttnWarps][256];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int G = p.q_heads / p.kv_heads, chunks = (G + kAttnGroup - 1) / kAttnGroup;
-  const int64_t item = blockIdx.x;
-  const int chunk = static_cast<int>(item % chunks), hk = static_cast<int>(item / chunks % p.kv_heads);
-  const int64_t row = item / chunks / p.kv_heads;
-  const int g0 = chunk * kAttnGroup, ng = min(kAttnGroup, G - g0);
-  const int seq = p.row_seq ? p.row_seq[row] : static_cast<int>(row);
-  int64_t len = p.lengths[row];
-  bool bad = false;
-  if (len > static_cast<int64_t>(p.max_pages) * p.page_size) {
-    len = static_cast<int64_t>(p.max_pages) * p.page_size;
-    bad = true;
-  }
-  if (len > 0 && (seq < 0 || seq >= p.num_seqs)) {
-    len = 0;
-    bad = true;
-  }
-  float q[kAttnGroup][NE], o[kAttnGroup][NE], m[kAttnGroup], l[kAttnGroup];
+
+  // ---- this block's run of tiles: [i0, i1) of T, in the order (row, unit, tile)
+  int64_t T, i0, i1;
+  int workers;
+  {
+    const int per = (p.M + kAttnThreads - 1) / kAttnThreads;
+    const int r0 = min(tid * per, p.M), r1 = min(r0 + per, p.M);
+    int64_t sum = 0;
+    bool bad = false;
+    for (int r = r0; r < r1; ++r) sum += max(1, (row_info(p, r, bad).len + CT - 1) / CT);
+    if (bad && blockIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
+    int64_t incl = sum;
 #pragma unroll
-  for (int g = 0; g < kAttnGroup; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int d = lane + 32 * e;
-      o[g][e] = 0.0f;
-      q[g][e] = g < ng && d < p.head_dim
-                    ? to_f32(static_cast<const T*>(p.Q)[row * p.ldq + static_cast<int64_t>(hk * G + g0 + g) * p.head_dim + d])
-                    : 0.0f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
     }
-  }
-  const float sk = sizeof(C) == 1 ? p.scale * *p.scale_k : p.scale;
-  for (int64_t t = w; t < len; t += kAttnWarps) {
-    const int page = p.page_table[static_cast<int64_t>(seq) * p.max_pages + t / p.page_size];
-    if (page < 0 || page >= p.num_pages) {
-      bad = true;
-      continue;
-    }
-    const int64_t at = ((static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size + t % p.page_size) * p.head_dim;
-    float k[NE], v[NE];
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int d = lane + 32 * e;
-      k[e] = d < p.head_dim ? to_f32(static_cast<const C*>(p.Kc)[at + d]) : 0.0f;
-      v[e] = d < p.head_dim ? to_f32(static_cast<const C*>(p.Vc)[at + d]) : 0.0f;
-    }
-#pragma unroll
-    for (int g = 0; g < kAttnGroup; ++g) {
-      float s = 0.0f;
-#pragma unroll
-      for (int e = 0; e < NE; ++e) s += q[g][e] * k[e];
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= sk;
-      const float m2 = fmaxf(m[g], s);
-      const float base = m2 == -INFINITY ? 0.0f : m2;
-      const float c = expf(m[g] - base), pr = expf(s - base);
-      m[g] = m2;
-      l[g] = l[g] * c + pr;
-#pragma unroll
-      for (int e = 0; e < NE; ++e) o[g][e] = o[g][e] * c + pr * v[e];
-    }
-  }
-  if (bad) atomicOr(&g_paged_status, kDevBadIndex);
-#pragma unroll
-  for (int g = 0; g < kAttnGroup; ++g)
-    if (lane == 0) {
-      s_m[w][g] = m[g];
-      s_l[w][g] = l[g];
-    }
-  const float sv = sizeof(C) == 1 ? *p.scale_v : 1.0f;
-#pragma unroll
-  for (int g = 0; g < kAttnGroup; ++g) {
+    if (lane == 31) s_scan[w] = incl;
     __syncthreads();
+    int64_t before = 0, total = 0;
 #pragma unroll
-    for (int e = 0; e < NE; ++e) s_o[w][lane + 32 * e] = o[g][e];
-    __syncthreads();
-    if (g >= ng) continue;
-    float mm = -INFINITY;
-    for (int x = 0; x < kAttnWarps; ++x) mm = fmaxf(mm, s_m[x][g]);
-    const float base = mm == -INFINITY ? 0.0f : mm;
-    float ll = 0.0f;
-    for (int x = 0; x < kAttnWarps; ++x) ll += s_l[x][g] * expf(s_m[x][g] - base);
-    const int64_t head = static_cast<int64_t>(hk) * G + g0 + g;
-    for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
-      float oo = 0.0f;
-      for (int x = 0; x < kAttnWarps; ++x) oo += s_o[x][d] * expf(s_m[x][g] - base);
-      static_cast<T*>(p.O)[(row * p.q_heads + head) * p.head_dim + d] =
-          from_f32<T>(ll == 0.0f ? 0.0f : oo / ll * sv);
+    for (int x = 0; x < kAttnWarps; ++x) {
+      if (x < w) before += s_scan[x];
+      total += s_scan[x];
     }
-    if (p.lse && threadIdx.x == 0) p.lse[row * p.q_heads + head] = ll == 0.0f ? -INFINITY : mm + logf(ll);
+    T = total * units;
+    workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(T / kMinTiles, static_cast<int64_t>(1))));
+    if (static_cast<int>(blockIdx.x) >= workers) return;
+    i0 = T * blockIdx.x / workers;
+    i1 = T * (blockIdx.x + 1) / workers;
+    int64_t at = (before + incl - sum) * units;  // first tile of this thread's rows
+    if (i0 >= at && i0 < at + sum * units) {
+      for (int r = r0; r < r1; ++r) {
+        const int nt = max(1, (row_info(p, r, bad).len + CT - 1) / CT);
+        if (i0 < at + static_cast<int64_t>(nt) * units) {
+          s_start[0] = r;
+          s_start[1] = static_cast<int>((i0 - at) / nt);
+          s_start[2] = static_cast<int>((i0 - at) % nt);
+          break;
+        }
+        at += static_cast<int64_t>(nt) * units;
+      }
+    }
+    __syncthreads();
   }
+  const int64_t n = i1 - i0;
+
+  // ---- the loads: page numbers one tile ahead, rows ST - 1 tiles ahead
+  Cursor in;
+  in.row = s_start[0];
+  in.h = s_start[1];
+  in.t = s_start[2];
+  in.enter(p, CT);
+  Cursor at = in;
+  int pg[KPL], slot[KPL];
+  bool bad_page = false;
+  auto look_up = [&]() {
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+      const int key = in.t * CT + w * KT + lane + 32 * j;
+      pg[j] = -1;
+      slot[j] = -1;  // no such key
+      if (lane + 32 * j < KT && key < in.len) {
+        const int q = key / p.page_size;
+        slot[j] = key - q * p.page_size;
+        pg[j] = __ldg(p.page_table + static_cast<int64_t>(in.seq) * p.max_pages + q);
+      }
+    }
+  };
+  auto issue = [&](int stage) {
+    const int hk = in.h / groups;
+    int64_t off[KPL];
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+      const bool ok = pg[j] >= 0 && pg[j] < p.num_pages && slot[j] >= 0;
+      bad_page |= !ok && slot[j] >= 0;
+      off[j] = ok ? ((static_cast<int64_t>(pg[j]) * p.kv_heads + hk) * p.page_size + slot[j]) * p.head_dim *
+                        static_cast<int64_t>(sizeof(C))
+                  : -1;
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) s_mask[w][stage][j] = mask;
+    }
+    const uint32_t dst = ring + stage * S::STAGE;
+    constexpr int LPR = CPR < 32 ? CPR : 32;  // lanes of a row
+#pragma unroll
+    for (int r0 = 0; r0 < KT; r0 += 32 / LPR) {
+      const int row = r0 + lane / LPR;
+      int64_t o = __shfl_sync(0xffffffffu, off[0], row & 31);
+      if constexpr (KPL == 2) {
+        const int64_t o2 = __shfl_sync(0xffffffffu, off[1], row & 31);
+        o = row < 32 ? o : o2;
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < CPR; c0 += LPR) {
+        const int c = c0 + lane % LPR;
+        if (c < chunks) {
+          const int64_t src = (o < 0 ? 0 : o) + c * 16;
+          const int to = staged<PITCH>(row, c);
+          cp_async16(dst + to, static_cast<const char*>(p.Kc) + src, o >= 0);
+          cp_async16(dst + KT * PITCH + to, static_cast<const char*>(p.Vc) + src, o >= 0);
+        }
+      }
+    }
+  };
+  look_up();
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) {
+    if (s < n) {
+      issue(s);
+      in.next(p, units, CT);
+      if (s + 1 < n) look_up();
+    }
+    cp_async_commit();
+  }
+
+  // ---- per-warp state.  mma: rows lane / 4 (and, WIDE, lane / 4 + 8); fp32:
+  // columns of this lane.
+  constexpr int OW = S::F32 ? RG * DP / 32 : DP / 2;
+  constexpr int NR = S::F32 ? RG : (WIDE ? 2 : 1);
+  constexpr int KS = DP / 16;
+  float o[OW], m[NR], l[NR];
+  uint32_t q[S::F32 ? 1 : KS * (WIDE ? 4 : 2)] = {};
+  float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)
+  float* s_q = reinterpret_cast<float*>(smem + S::RING + S::JOIN);  // fp32: [RG][DP]
+  float* s_p = s_q + RG * DP + w * KT * RG;                         // fp32: [KT][RG] of this warp
+  const float sk = S::E4M3 ? p.scale * *p.scale_k : p.scale;
+  const float sv = S::E4M3 ? *p.scale_v : 1.0f;
+
+  auto begin_item = [&]() {
+    const int hk = at.h / groups, g0 = (at.h % groups) * gsize, ng = min(gsize, G - g0);
+    const E* src = static_cast<const E*>(p.Q) + at.row * p.ldq + static_cast<int64_t>(hk * G + g0) * p.head_dim;
+#pragma unroll
+    for (int i = 0; i < OW; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+      s2[r] = sk * kLog2e;
+    }
+    if constexpr (S::F32) {
+      __syncthreads();
+      for (int i = tid; i < RG * DP; i += kAttnThreads) {
+        const int g = i / DP, d = i % DP;
+        s_q[i] = g < ng && d < p.head_dim ? src[g * p.head_dim + d] : 0.0f;
+      }
+      __syncthreads();
+    } else {
+      constexpr int QR = WIDE ? 4 : 2;
+      const int c4 = lane & 3;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int g = (lane >> 2) + 8 * r;
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(src + static_cast<int64_t>(g) * p.head_dim);
+        float big = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            // e4m3: the 16 columns of a step in the order of the staged bytes (see the products)
+            const int d = ks * 16 + (S::E4M3 ? 4 * c4 + 2 * x : 2 * c4 + 8 * x);
+            const uint32_t v = g < ng && d < p.head_dim ? __ldg(row + d / 2) : 0u;
+            q[ks * QR + (WIDE ? 2 * x + r : x)] = v;
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        if constexpr (S::E4M3) {
+          // q in f16 beside the keys' exact f16 values: each head's q is scaled by a power of two to a largest
+          // value in [2^14, 2^15), so what f16 cannot hold lies 2^-28 and more below it
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          const int ex = big > 0.0f ? min(max(14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127), -112), 126) : 0;
+          const float up = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t& v = q[ks * QR + (WIDE ? 2 * x + r : x)];
+              const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+              v = pack2<true>(f.x * up, f.y * up);
+            }
+          s2[r] = sk * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        }
+      }
+    }
+  };
+
+  // One tile of the products on the tensor cores.
+  auto tile_mma = [&](int stage) {
+    constexpr int NT = KT / 8, QR = WIDE ? 4 : 2;
+    const uint32_t kb = ring + stage * S::STAGE, vb = kb + KT * PITCH;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[t][x] = 0.0f;
+    auto a_of = [&](int ks, int x) -> uint32_t { return WIDE ? q[ks * QR + x] : (x & 1) ? 0u : q[ks * QR + x / 2]; };
+    if constexpr (!S::E4M3) {
+      // two blocks of 8 keys and 16 columns by one ldmatrix
+#pragma unroll
+      for (int t = 0; t < NT; t += 2)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[4];
+          ldmatrix4<false>(b, kb + staged<PITCH>(t * 8 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
+          mma16816<F16>(s[t], a_of(ks, 0), a_of(ks, 1), a_of(ks, 2), a_of(ks, 3), b[0], b[1]);
+          mma16816<F16>(s[t + 1], a_of(ks, 0), a_of(ks, 1), a_of(ks, 2), a_of(ks, 3), b[2], b[3]);
+        }
+    } else {
+      // a lane's 4 bytes are 4 consecutive columns: the pairs (0, 1) and (2, 3) are taken as the instruction's
+      // columns 2 c4 and 2 c4 + 8, for q and k alike
+#pragma unroll
+      for (int t = 0; t < NT; t += 2)
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t b[4];
+          ldmatrix4<false>(b, kb + staged<PITCH>(t * 8 + (lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int tt = t + u / 2, kk = ks + (u & 1);
+            mma16816<F16>(s[tt], a_of(kk, 0), a_of(kk, 1), a_of(kk, 2), a_of(kk, 3), e4m3x2_f16x2(b[u]),
+                          e4m3x2_f16x2(b[u] >> 16));
+          }
+        }
+    }
+    // weights
+    const uint32_t mask0 = s_mask[w][stage][0], mask1 = KPL == 2 ? s_mask[w][stage][1] : 0u;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float big = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = t * 8 + 2 * (lane & 3) + x;
+          const bool there = ((key < 32 ? mask0 : mask1) >> (key & 31)) & 1u;
+          float& v = s[t][2 * r + x];
+          v = there ? v * s2[r] : -INFINITY;
+          big = fmaxf(big, v);
+        }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      if (__any_sync(0xffffffffu, big > m[r])) {
+        const float mn = fmaxf(m[r], big);
+        const float c = mn == -INFINITY ? 1.0f : ex2_approx(m[r] - mn);
+        m[r] = mn;
+        l[r] *= c;
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+          if constexpr (WIDE) {
+            o[4 * i + 2 * r] *= c;
+            o[4 * i + 2 * r + 1] *= c;
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[4 * i + x] *= c;
+          }
+        }
+      }
+      const float base = m[r] == -INFINITY ? 0.0f : m[r];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float& v = s[t][2 * r + x];
+          v = ex2_approx(v - base);
+          l[r] += v;
+        }
+    }
+    // o += p v.  With up to 8 heads the lower 8 rows of the instruction carry the rest of p's rounding to 16 bits,
+    // so p keeps 16 bits or more; with more heads p is rounded once (bf16: 2^-9 of each weight on average a
+    // quarter of it, below the output's own rounding)
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; ++kk) {
+      uint32_t a[4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float(&v)[4] = s[2 * kk + x];
+        a[2 * x] = pack2<F16>(v[0], v[1]);
+        if constexpr (WIDE) {
+          a[2 * x + 1] = pack2<F16>(v[2], v[3]);
+        } else {
+          float2 f;
+          if constexpr (F16)
+            f = __half22float2(*reinterpret_cast<const __half2*>(&a[2 * x]));
+          else
+            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a[2 * x]));
+          a[2 * x + 1] = pack2<F16>(v[0] - f.x, v[1] - f.y);
+        }
+      }
+      const int row = kk * 16 + (lane & 15);
+      if constexpr (!S::E4M3) {
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          uint32_t b[4];
+          ldmatrix4<true>(b, vb + staged<PITCH>(row, d * 2 + (lane >> 4)));
+          float(&o0)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * d);
+          float(&o1)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * d + 4);
+          mma16816<F16>(o0, a[0], a[1], a[2], a[3], b[0], b[1]);
+          mma16816<F16>(o1, a[0], a[1], a[2], a[3], b[2], b[3]);
+        }
+      } else {
+        // a transposed pair of bytes is two columns of one key: the even columns of 16 make one block of the
+        // output, the odd ones another
+#pragma unroll
+        for (int d = 0; d < DP / 16; d += 2) {
+          uint32_t b[4];
+          ldmatrix4<true>(b, vb + staged<PITCH>(row, d + (lane >> 4)));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x0 = e4m3x2_f16x2(b[2 * u]), x1 = e4m3x2_f16x2(b[2 * u] >> 16);
+            const uint32_t y0 = e4m3x2_f16x2(b[2 * u + 1]), y1 = e4m3x2_f16x2(b[2 * u + 1] >> 16);
+            float(&o0)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * (d + u));
+            float(&o1)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * (d + u) + 4);
+            mma16816<F16>(o0, a[0], a[1], a[2], a[3], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
+            mma16816<F16>(o1, a[0], a[1], a[2], a[3], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+          }
+        }
+      }
+    }
+  };
+
+  // One tile in fp32: 32 / KT lanes share a key's columns, then each lane takes DP / 32 columns of o.
+  auto tile_f32 = [&](int stage) {
+    constexpr int PARTS = 32 / (KT < 32 ? KT : 32), NC = DP / 32;
+    const uint8_t* kb = smem + w * ST * S::STAGE + stage * S::STAGE;
+    const uint8_t* vb = kb + KT * PITCH;
+    const int key = lane % KT, part = lane / KT;
+    float s[RG];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) s[g] = 0.0f;
+#pragma unroll 4
+    for (int c = part; c < CPR; c += PARTS) {
+      const float4 k = *reinterpret_cast<const float4*>(kb + staged<PITCH>(key, c));
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        const float4 x = *reinterpret_cast<const float4*>(s_q + g * DP + 4 * c);
+        s[g] += (k.x * x.x + k.y * x.y) + (k.z * x.z + k.w * x.w);
+      }
+    }
+    const bool there = (s_mask[w][stage][0] >> key) & 1u;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+#pragma unroll
+      for (int x = KT; x < 32; x <<= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], x);
+      s[g] = there ? s[g] * s2[g] : -INFINITY;
+      float big = s[g];
+#pragma unroll
+      for (int x = 1; x < KT; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+      if (big > m[g]) {  // the same in every lane
+        const float c = ex2_approx(m[g] - big);
+        m[g] = big;
+        l[g] *= c;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o[g * NC + i] *= c;
+      }
+      s[g] = ex2_approx(s[g] - (m[g] == -INFINITY ? 0.0f : m[g]));
+      if (part == 0) {
+        l[g] += s[g];
+        s_p[key * RG + g] = s[g];
+      }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int t = 0; t < KT; ++t) {
+      float v[NC];
+      if constexpr (NC == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(vb + staged<PITCH>(t, lane / 2) + (lane & 1) * 8);
+        v[0] = x.x;
+        v[1] = x.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(vb + staged<PITCH>(t, lane + 32 * i));
+          v[4 * i] = x.x;
+          v[4 * i + 1] = x.y;
+          v[4 * i + 2] = x.z;
+          v[4 * i + 3] = x.w;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        const float pr = s_p[t * RG + g];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o[g * NC + i] += pr * v[i];
+      }
+    }
+    __syncwarp();
+  };
+
+  // This lane's elements of o: f(row, column, value index); mma without WIDE: value i and i + 2 are one element.
+  auto each = [&](auto&& f) {
+    if constexpr (S::F32) {
+      constexpr int NC = DP / 32;
+#pragma unroll
+      for (int g = 0; g < RG; ++g)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) f(g, NC == 2 ? 2 * lane + i : 4 * lane + 128 * (i / 4) + i % 4, g * NC + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int c4 = lane & 3;
+            const int d = S::E4M3 ? (i / 2) * 16 + 4 * c4 + 2 * x + (i & 1) : i * 8 + 2 * c4 + x;
+            f((lane >> 2) + 8 * r, d, 4 * i + 2 * r + x);
+          }
+    }
+  };
+  // (m, l, o) of this warp into or out of join buffer b
+  auto put = [&](int b) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = S::F32 ? r : (lane >> 2) + 8 * r;
+      if (S::F32 ? lane == 0 : (lane & 3) == 0) {
+        s_ml[b][row][0] = m[r];
+        s_ml[b][row][1] = l[r];
+      }
+    }
+    each([&](int row, int d, int i) { s_o[(b * RG + row) * DP + d] = o[i]; });
+  };
+  auto take = [&](int b) {
+    float c[NR], c2[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = S::F32 ? r : (lane >> 2) + 8 * r;
+      const float m2 = s_ml[b][row][0], mn = fmaxf(m[r], m2), base = mn == -INFINITY ? 0.0f : mn;
+      c[r] = ex2_approx(m[r] - base);
+      c2[r] = ex2_approx(m2 - base);
+      m[r] = mn;
+      l[r] = l[r] * c[r] + s_ml[b][row][1] * c2[r];
+    }
+    each([&](int row, int d, int i) {
+      const int r = S::F32 ? i / (DP / 32) : (i >> 1) & (NR - 1);
+      o[i] = o[i] * c[r] + s_o[(b * RG + row) * DP + d] * c2[r];
+    });
+  };
+
+  // Counters [kMaxWorkers], then per block two parts of (m, l) [gsize] and o [gsize][head_dim]
+  unsigned* counters = static_cast<unsigned*>(p.workspace);
+  const int part_floats = gsize * (p.head_dim + 4);
+  float* parts = reinterpret_cast<float*>(counters + kMaxWorkers);
+
+  auto write_row = [&](int r, int d, float4 v, float mm, float ll) {
+    const int hk = at.h / groups, g0 = (at.h % groups) * gsize;
+    const int64_t head = static_cast<int64_t>(at.row) * p.q_heads + hk * G + g0 + r;
+    const float inv = ll == 0.0f ? 0.0f : sv / ll;
+    v.x = ll == 0.0f ? 0.0f : v.x * inv;
+    v.y = ll == 0.0f ? 0.0f : v.y * inv;
+    v.z = ll == 0.0f ? 0.0f : v.z * inv;
+    v.w = ll == 0.0f ? 0.0f : v.w * inv;
+    E* dst = static_cast<E*>(p.O) + head * p.head_dim + d;
+    if constexpr (S::F32) {
+      *reinterpret_cast<float4*>(dst) = v;
+    } else {
+      uint2 u = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+      *reinterpret_cast<uint2*>(dst) = u;
+    }
+    if (p.lse && d == 0) p.lse[head] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  };
+
+  // The warps' parts of tiles [first, i] of the item at `at` joined, and written out or left for the last block.
+  auto end_item = [&](int64_t first_tile, int64_t last_tile) {  // of the whole item, among all T
+    if constexpr (!S::F32) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      }
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+          o[4 * i] += o[4 * i + 2];
+          o[4 * i + 1] += o[4 * i + 3];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < RG; ++g)
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], x);
+    }
+    const int ng = min(gsize, G - (at.h % groups) * gsize), vecs = p.head_dim / 4;
+    if (w >= 2) put(w - 2);
+    __syncthreads();
+    if (w < 2) take(w);
+    __syncthreads();
+    if (w < 2) put(w);
+    __syncthreads();
+    auto both = [&](int r, int d, float& mm, float& ll) {
+      const float m0 = s_ml[0][r][0], m1 = s_ml[1][r][0];
+      mm = fmaxf(m0, m1);
+      const float base = mm == -INFINITY ? 0.0f : mm, c0 = ex2_approx(m0 - base), c1 = ex2_approx(m1 - base);
+      ll = s_ml[0][r][1] * c0 + s_ml[1][r][1] * c1;
+      const float4 a = *reinterpret_cast<const float4*>(s_o + r * DP + d);
+      const float4 b = *reinterpret_cast<const float4*>(s_o + (RG + r) * DP + d);
+      return make_float4(a.x * c0 + b.x * c1, a.y * c0 + b.y * c1, a.z * c0 + b.z * c1, a.w * c0 + b.w * c1);
+    };
+    // blocks that share the item: the one of its first tile to the one of its last
+    auto worker_of = [&](int64_t i) { return static_cast<int>(((i + 1) * workers - 1) / T); };
+    const bool whole = first_tile >= i0 && last_tile < i1;
+    if (whole) {
+      for (int i = tid; i < ng * vecs; i += kAttnThreads) {
+        const int r = i / vecs, d = (i % vecs) * 4;
+        float mm, ll;
+        const float4 v = both(r, d, mm, ll);
+        write_row(r, d, v, mm, ll);
+      }
+    } else {
+      const int wf = worker_of(first_tile), wl = worker_of(last_tile);
+      auto part_of = [&](int c) {  // an item begun in block c behind its first tile is that block's second part
+        const int second = c == wf && first_tile > T * c / workers;
+        return parts + (static_cast<int64_t>(c) * 2 + second) * part_floats;
+      };
+      float* mine = part_of(blockIdx.x);
+      for (int i = tid; i < ng * vecs; i += kAttnThreads) {
+        const int r = i / vecs, d = (i % vecs) * 4;
+        float mm, ll;
+        const float4 v = both(r, d, mm, ll);
+        __stcg(reinterpret_cast<float4*>(mine + gsize * 4 + r * p.head_dim + d), v);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(mine + r * 4), make_float2(mm, ll));
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned arrived = atomicAdd(counters + wf, 1u);
+        s_last = arrived == static_cast<unsigned>(wl - wf);
+        if (s_last) counters[wf] = 0;  // ready for the next call
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int i = tid; i < ng * vecs; i += kAttnThreads) {
+          const int r = i / vecs, d = (i % vecs) * 4;
+          float mm = -INFINITY, ll = 0.0f;
+          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (int c = wf; c <= wl; ++c) {
+            const float* part = part_of(c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + r * 4));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + gsize * 4 + r * p.head_dim + d));
+            const float mn = fmaxf(mm, ml.x), base = mn == -INFINITY ? 0.0f : mn;
+            const float c0 = ex2_approx(mm - base), c1 = ex2_approx(ml.x - base);
+            mm = mn;
+            ll = ll * c0 + ml.y * c1;
+            acc = make_float4(acc.x * c0 + v.x * c1, acc.y * c0 + v.y * c1, acc.z * c0 + v.z * c1,
+                              acc.w * c0 + v.w * c1);
+          }
+          write_row(r, d, acc, mm, ll);
+        }
+      }
+    }
+    __syncthreads();  // the join buffers are free again
+  };
+
+  int64_t item = i0 - at.t;  // first tile, among all T, of the item at `at`
+  begin_item();
+  int stage = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    cp_async_wait<ST - 2>();
+    __syncwarp();
+    if (i + ST - 1 < n) {
+      issue(stage == 0 ? ST - 1 : stage - 1);
+      in.next(p, units, CT);
+      if (i + ST < n) look_up();
+    }
+    cp_async_commit();
+    bool any = s_mask[w][stage][0] != 0u;
+    if constexpr (KPL == 2) any |= s_mask[w][stage][1] != 0u;
+    if (any) {
+      if constexpr (S::F32)
+        tile_f32(stage);
+      else
+        tile_mma(stage);
+    }
+    if (at.t + 1 == at.nt || i + 1 == n) {
+      end_item(item, item + at.nt - 1);
+      item += at.nt;
+      at.next(p, units, CT);
+      if (i + 1 < n) begin_item();
+    } else {
+      ++at.t;
+    }
+    if (++stage == ST) stage = 0;
+  }
+  cp_async_wait<0>();
+  if (bad_page) atomicOr(&g_paged_status, kDevBadIndex);
+}
+
+template <class T, class C, int DP, bool WIDE>
+cudaError_t run_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
+  using S = AttnShape<T, C, DP, WIDE>;
+  const void* k = reinterpret_cast<const void*>(attention_kernel<T, C, DP, WIDE>);
+  static std::atomic<uint64_t> configured{0};  // a bit for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  const int G = p.q_heads / p.kv_heads;
+  const int64_t units = static_cast<int64_t>(p.kv_heads) * ((G + S::RG - 1) / S::RG);
+  const int64_t tiles = (static_cast<int64_t>(p.max_pages) * p.page_size + S::CT - 1) / S::CT;
+  int64_t grid = static_cast<int64_t>(device_sm_count()) * S::CTAS;
+  if (grid > kMaxWorkers) grid = kMaxWorkers;
+  // no more blocks than the page table has room for
+  if (tiles < grid && p.M * units < grid && tiles * p.M * units < grid) grid = tiles * p.M * units;
+  void* args[] = {const_cast<AttnParams*>(&p)};
+  return launch_ex(k, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), S::SMEM, s, pdl, args);
+}
+
+template <class T, class C>
+cudaError_t pick_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
+  const bool wide = p.q_heads / p.kv_heads > (sizeof(T) == 4 ? 1 : 8);
+  if (p.head_dim <= 64) return wide ? run_attention<T, C, 64, true>(p, s, pdl) : run_attention<T, C, 64, false>(p, s, pdl);
+  if (p.head_dim <= 128)
+    return wide ? run_attention<T, C, 128, true>(p, s, pdl) : run_attention<T, C, 128, false>(p, s, pdl);
+  return wide ? run_attention<T, C, 256, true>(p, s, pdl) : run_attention<T, C, 256, false>(p, s, pdl);
 }
 
 }  // namespace
@@ -201,16 +885,16 @@ cudaError_t launch_paged_append(const AppendParams& p, int64_t M, bool f32, bool
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl) {
-  const int G = p.q_heads / p.kv_heads;
-  const int64_t items = static_cast<int64_t>(p.M) * p.kv_heads * ((G + kAttnGroup - 1) / kAttnGroup);
-  const void* k = f32    ? reinterpret_cast<const void*>(attention_kernel<float, float>)
-                  : e4m3 ? reinterpret_cast<const void*>(attention_kernel<__nv_bfloat16, __nv_fp8_e4m3>)
-                         : reinterpret_cast<const void*>(attention_kernel<__nv_bfloat16, __nv_bfloat16>);
-  void* args[] = {const_cast<AttnParams*>(&p)};
-  return launch_ex(k, dim3(static_cast<unsigned>(items)), dim3(32 * kAttnWarps), 0, s, pdl, args);
+  return f32    ? pick_attention<float, float>(p, s, pdl)
+         : e4m3 ? pick_attention<__nv_bfloat16, __nv_fp8_e4m3>(p, s, pdl)
+                : pick_attention<__nv_bfloat16, __nv_bfloat16>(p, s, pdl);
 }
 
-int64_t paged_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim) { return 16; }
+// Counters and two parts of at most min(G, 16) heads for each block.
+int64_t paged_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
+  const int G = q_heads / kv_heads, rows = G < 16 ? G : 16;
+  return kMaxWorkers * (4 + 2 * static_cast<int64_t>(rows) * (head_dim + 4) * 4);
+}
 
 unsigned read_clear_status_paged() {
   unsigned v = 0, zero = 0;
