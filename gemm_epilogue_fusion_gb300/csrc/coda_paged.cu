@@ -24,66 +24,141 @@ namespace {
 // by read_clear_status_paged().
 __device__ unsigned g_paged_status;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <class T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// One thread per pair of a row's columns.
-template <class T, class C>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int half = p.head_dim / 2, heads = p.q_heads + 2 * p.kv_heads;
-  const int64_t i = blockIdx.x;
-  const int pos = p.positions[i];
-  if (pos < 0) return;
-  const int seq = p.row_seq ? p.row_seq[i] : static_cast<int>(i);
-  int page = -1;
-  if (seq >= 0 && seq < p.num_seqs && pos / p.page_size < p.max_pages)
-    page = p.page_table[static_cast<int64_t>(seq) * p.max_pages + pos / p.page_size];
-  if (page < 0 || page >= p.num_pages) {
-    if (threadIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
-    return;
-  }
-  const T* z = static_cast<const T*>(p.Z) + i * heads * p.head_dim;
-  for (int e = threadIdx.x; e < heads * half; e += blockDim.x) {
-    const int h = e / half, j = e % half;
-    float a = to_f32(z[h * p.head_dim + 2 * j]), b = to_f32(z[h * p.head_dim + 2 * j + 1]);
-    if (p.rotate && h < p.q_heads + p.kv_heads) {
-      const int turn = static_cast<int>((p.turn[j] * static_cast<uint64_t>(pos)) >> 32);
-      float s, c;
-      sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
-      const float x = a;
-      a = x * c - b * s;
-      b = x * s + b * c;
-    }
-    if (h < p.q_heads) {
-      if (p.Q == nullptr) continue;
-      T* q = static_cast<T*>(p.Q) + (i * p.q_heads + h) * p.head_dim + 2 * j;
-      q[0] = from_f32<T>(a);
-      q[1] = from_f32<T>(b);
-      continue;
-    }
-    const bool is_v = h >= p.q_heads + p.kv_heads;
-    const int hk = h - p.q_heads - (is_v ? p.kv_heads : 0);
-    const int64_t at = ((static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size + pos % p.page_size) *
-                           p.head_dim + 2 * j;
-    C* c = static_cast<C*>(is_v ? p.Vc : p.Kc) + at;
-    if constexpr (sizeof(C) == 1) {
-      const float s = is_v ? *p.scale_v : *p.scale_k;
-      *reinterpret_cast<uint16_t*>(c) = to_e4m3x2<false>(a, b, s, 0.0f);
-    } else {
-      c[0] = from_f32<C>(a);
-      c[1] = from_f32<C>(b);
+// 16 bytes of a row as fp32 values, and back.
+template <class E>
+__device__ __forceinline__ void unpack(const uint4& w, float (&f)[16 / sizeof(E)]) {
+  if constexpr (sizeof(E) == 4) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  } else {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = __bfloat1622float2(h[e]);
+      f[2 * e] = t.x;
+      f[2 * e + 1] = t.y;
     }
   }
 }
+template <class E>
+__device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
+  uint4 w;
+  if constexpr (sizeof(E) == 4) {
+    w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  } else {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+  }
+  return w;
+}
 
+// ------------------------------------------------------------------- append ----
+// One block per row, one thread per 16-byte chunk of a head: a thread keeps its
+// chunk's columns for all the heads it takes, so the sines and cosines of its
+// pairs are computed once a row.  The angle of pair j at position pos is the
+// fraction of a turn turn[j] * pos / 2^64, an exact product that wraps by whole
+// turns by itself; its upper 32 bits go to fp32 (2^-25 of half a turn).  bf16
+// takes the sine and cosine of the special-function unit (2^-21 of 1 on this
+// range, a 32nd of the output's rounding), fp32 the accurate ones.
+// Bound by the bytes of Z, Q and the new slots; the loads of a row's heads are
+// issued before its position and page are known.
+constexpr int kAppendThreads = 128, kAppendHeads = 6;  // heads of a thread in flight
+
+template <class E, class C>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int VEC = 16 / sizeof(E);
+  const int chunks = p.head_dim / VEC, heads = p.q_heads + 2 * p.kv_heads, lanes = kAppendThreads / chunks;
+  const int c = threadIdx.x % chunks, h0 = threadIdx.x / chunks;
+  const int64_t i = blockIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (h0 >= lanes) return;
+  const int pos = p.positions[i];
+  const int seq = p.row_seq ? p.row_seq[i] : static_cast<int>(i);
+  const uint4* z = reinterpret_cast<const uint4*>(static_cast<const E*>(p.Z) + i * heads * p.head_dim) + c;
+  float s[VEC / 2], co[VEC / 2], inv_k = 0.0f, inv_v = 0.0f, sk = 1.0f, sv = 1.0f;
+  bool fast = true;
+  if constexpr (sizeof(C) == 1) {
+    sk = *p.scale_k;
+    sv = *p.scale_v;
+    fast = e4m3_fast_scale(sk) && e4m3_fast_scale(sv);
+    inv_k = __frcp_rn(sk);
+    inv_v = __frcp_rn(sv);
+  }
+  int64_t slot = -1;  // row of the caches for head 0; -2: an index out of range
+  for (int hb = h0; hb < heads; hb += lanes * kAppendHeads) {
+    uint4 w[kAppendHeads];
+#pragma unroll
+    for (int u = 0; u < kAppendHeads; ++u) {
+      const int h = hb + u * lanes;
+      if (h < heads) w[u] = __ldg(z + static_cast<int64_t>(h) * chunks);
+    }
+    if (hb == h0) {
+      if (pos < 0) return;
+      int page = -1;
+      if (seq >= 0 && seq < p.num_seqs && pos / p.page_size < p.max_pages)
+        page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.max_pages + pos / p.page_size);
+      if (p.rotate) {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+          const int turn = static_cast<int>((p.turn[c * (VEC / 2) + e] * static_cast<uint64_t>(pos)) >> 32);
+          const float half_turns = static_cast<float>(turn) * 0x1p-31f;
+          if constexpr (sizeof(E) == 4)
+            sincospif(half_turns, &s[e], &co[e]);
+          else
+            __sincosf(half_turns * 3.14159265358979f, &s[e], &co[e]);
+        }
+      }
+      if (page < 0 || page >= p.num_pages) {
+        if (threadIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
+        return;
+      }
+      slot = static_cast<int64_t>(page) * p.kv_heads * p.page_size + pos % p.page_size;
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendHeads; ++u) {
+      const int h = hb + u * lanes;
+      if (h >= heads) break;
+      if (h < p.q_heads && p.Q == nullptr) continue;
+      const bool is_v = h >= p.q_heads + p.kv_heads;
+      float f[VEC];
+      unpack<E>(w[u], f);
+      if (p.rotate && !is_v) {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+          const float a = f[2 * e], b = f[2 * e + 1];
+          f[2 * e] = a * co[e] - b * s[e];
+          f[2 * e + 1] = a * s[e] + b * co[e];
+        }
+      }
+      if (h < p.q_heads) {
+        reinterpret_cast<uint4*>(static_cast<E*>(p.Q) + (i * p.q_heads + h) * p.head_dim)[c] = pack<E>(f);
+        continue;
+      }
+      const int hk = h - p.q_heads - (is_v ? p.kv_heads : 0);
+      C* dst = static_cast<C*>(is_v ? p.Vc : p.Kc) + (slot + static_cast<int64_t>(hk) * p.page_size) * p.head_dim +
+               c * VEC;
+      if constexpr (sizeof(C) == 1) {
+        const float sc = is_v ? sv : sk, inv = is_v ? inv_v : inv_k;
+        uint32_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t lo = fast ? to_e4m3x2<true>(f[4 * j], f[4 * j + 1], sc, inv)
+                                   : to_e4m3x2<false>(f[4 * j], f[4 * j + 1], sc, inv);
+          const uint32_t hi = fast ? to_e4m3x2<true>(f[4 * j + 2], f[4 * j + 3], sc, inv)
+                                   : to_e4m3x2<false>(f[4 * j + 2], f[4 * j + 3], sc, inv);
+          o[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = pack<C>(f);
+      }
+    }
+  }
+}
 
 // ---------------------------------------------------------------- attention ----
 // One new token per row, flash-decoding style: o = sum_t p_t v_t / sum_t p_t,
@@ -881,7 +956,7 @@ cudaError_t launch_paged_append(const AppendParams& p, int64_t M, bool f32, bool
                   : e4m3 ? reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_fp8_e4m3>)
                          : reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_bfloat16>);
   void* args[] = {const_cast<AppendParams*>(&p)};
-  return launch_ex(k, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, pdl, args);
+  return launch_ex(k, dim3(static_cast<unsigned>(M)), dim3(kAppendThreads), 0, s, pdl, args);
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl) {

@@ -444,7 +444,7 @@ CODA_API coda_status coda_gemm_swiglu_backward(const void* dOut, const void* Wt,
  *   Z         [M, (q_heads + 2 kv_heads) * head_dim], dtype: query heads, key
  *             heads, value heads
  *   positions [M] int32: the position p of each row.  p < 0: a padded row,
- *             nothing of it is read or written.
+ *             nothing is written for it.
  *   base      0: Z's heads are taken as they are (already rotated by the
  *             GEMM's epilogue); else finite, > 1: pair j of every query and
  *             key head turns by p * base^(-2j / head_dim).  The angle is kept
