@@ -1280,6 +1280,8 @@ coda_status coda_logprobs_backward(const void* logits, int64_t ld, const int32_t
   g_msg[0] = 0;
   TRY(check_logits(M, V, ld, "ld", dtype));
   TRY(check_logits(M, V, ldd, "ldd", dtype));
+  REQUIRE(M * coda::logprobs_backward_blocks(V, dtype == CODA_F32) < INT32_MAX,
+          "M = %" PRId64 ", V = %" PRId64 ": too many blocks for one launch", M, V);
   if (M == 0) return CODA_OK;
   TRY(check_ptr(logits, "logits"));
   TRY(check_scalar_ptr(targets, "targets"));

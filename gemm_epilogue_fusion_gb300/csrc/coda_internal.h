@@ -205,6 +205,7 @@ struct LogprobsParams {
   float* top_logp;  // [M, top]
   int32_t* top_ids;
   int V, top;
+  int ranks;  // blocks that share a row (set by the launcher)
 };
 struct LogprobsGradParams {
   const void* logits;
@@ -217,9 +218,11 @@ struct LogprobsGradParams {
   void* dlogits;
   int64_t ldd;
   int V;
+  int blocks;  // blocks of a row (set by the launcher)
 };
 cudaError_t launch_logprobs(const LogprobsParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl);
 cudaError_t launch_logprobs_backward(const LogprobsGradParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl);
+int64_t logprobs_backward_blocks(int64_t V, bool f32);
 unsigned read_clear_status_logprobs();
 
 // Host helpers (coda_abi.cu).

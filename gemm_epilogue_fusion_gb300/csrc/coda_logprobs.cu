@@ -2,6 +2,7 @@
 // alternatives, and their gradient:
 //   lse = log sum_j exp x_j,  logp = x_t - lse,  H = lse - sum_j p_j x_j
 //   dx_j = dlogp ([j = t] - p_j) - dH p_j (x_j - lse + H),  p_j = exp(x_j - lse)
+// Nothing here waits on another block, but for the blocks of one cluster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -14,138 +15,470 @@
 namespace coda {
 namespace {
 
+// Status word of this translation unit (kDevBadIndex), read back and cleared
+// by read_clear_status_logprobs().
 __device__ unsigned g_logprobs_status;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float red[32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0f;
-  for (int w = 0; w < kThreads / 32; ++w) v += red[w];
-  return v;
+// The larger of two values, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
-// Order of two candidates: the larger value first, then the lower index; NaN
-// counts as the largest value.  64-bit keys that compare the same way.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t j) {
-  uint32_t b = __float_as_uint(x + 0.0f);
-  b = x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return (static_cast<uint64_t>(b) << 32) | (~j);
-}
-
-__device__ __forceinline__ uint64_t block_max_key(uint64_t v) {
-  __shared__ uint64_t red[32];
+// 16 bytes of logits as pairs of fp32 values.
+template <class E>
+__device__ __forceinline__ void pairs(const uint4& w, float2 (&f)[8 / sizeof(E)]) {
+  if constexpr (sizeof(E) == 4) {
+    f[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    f[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+  } else {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u > v ? u : v;
+    for (int e = 0; e < 4; ++e) f[e] = __bfloat1622float2(h[e]);
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  for (int w = 0; w < kThreads / 32; ++w) v = red[w] > v ? red[w] : v;
-  return v;
 }
 
-// One block per row: the maximum, then the sums, then the alternatives one by one.
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+// The largest of 16 bytes of logits.
+template <class E>
+__device__ __forceinline__ float largest(const uint4& w) {
+  if constexpr (sizeof(E) == 4) {
+    return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                   max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+}
+
+// Vector v of a row of V logits; elements behind the row are -inf.
+template <class E>
+__device__ __forceinline__ uint4 load_vec(const E* x, int v, int V) {
+  constexpr int VEC = 16 / sizeof(E);
+  if ((v + 1) * VEC <= V) return __ldcs(reinterpret_cast<const uint4*>(x) + v);
+  uint4 w;
+  E* e = reinterpret_cast<E*>(&w);
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    const int j = v * VEC + k;
+    if constexpr (sizeof(E) == 4)
+      e[k] = j < V ? x[j] : -INFINITY;
+    else
+      e[k] = j < V ? x[j] : __ushort_as_bfloat16(0xFF80);
+  }
+  return w;
+}
+
+// Order of the alternatives: the larger value first (NaN counts as the
+// largest), then the lower index.  32-bit keys order the values; 64-bit keys
+// with the index's complement below are distinct.  No value has the key 0.
+__device__ __forceinline__ uint32_t value_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 is 0
+  return x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : (k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+// Partial sums of a set of logits relative to their largest m: s = sum 2^d,
+// t = sum d 2^d with d = (x - m) log2 e.  -inf has no part in either.
+struct Sums {
+  float m, s, t;
+  // the same sums relative to a larger (or NaN) maximum
+  __device__ __forceinline__ void raise(float mn) {
+    if (s != 0.0f) {
+      const float d = (m - mn) * kLog2e, c = ex2_approx(d);
+      t = c == 0.0f ? 0.0f : (t + s * d) * c;
+      s *= c;
+    }
+    m = mn;
+  }
+  __device__ __forceinline__ void add(const Sums& o) {
+    const float mn = max_nan(m, o.m);
+    Sums b = o;
+    raise(mn);
+    b.raise(mn);
+    s += b.s;
+    t += b.t;
+  }
+};
+
+constexpr int kCandidates = 1024;
+constexpr int kMaxCluster = 8;
+
+template <int NT>
+struct LogprobsShared {
+  Sums warp[NT / 32];
+  uint32_t key[NT];       // each thread's largest value
+  int owner[NT];          // threads whose largest value reaches the bound
+  uint32_t bound;
+  int owners, found;
+  uint64_t cand[kCandidates];
+  uint64_t red[NT / 32];
+  // what the cluster's first block collects
+  Sums part;
+  uint64_t best[kMaxTop];
+};
+
+// One pass over a row (or, in a cluster, over a part of it) with a running
+// maximum, sum and sum of d 2^d per thread, joined at the end.
+//
+// The alternatives cost the pass nothing: each thread knows its own largest
+// value, and the top-th largest of those is a bound that at least `top`
+// elements reach.  Only threads whose largest value reaches it can hold an
+// alternative (with distinct values `top` of them, each with 1 / NT of the
+// row), so their elements are read once more, from L2 as a rule: 20 of 512
+// threads are 4% of the row.  The few elements that reach the bound are ranked
+// by counting.  If ties leave more than kCandidates of them, the alternatives
+// are found one by one instead.
+//
+// Bound by the row's bytes.  bf16 costs about 5 issue slots an element (the
+// arithmetic is packed in pairs) of the 11 that the HBM rate leaves.
+template <class E, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+  constexpr int VEC = 16 / sizeof(E), U = 4;
+  __shared__ LogprobsShared<NT> sh;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0, ranks = CLUSTER ? p.ranks : 1;
+  const int64_t i = blockIdx.x / ranks;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i = blockIdx.x;
-  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
-  uint64_t best = 0;
-  for (int j = threadIdx.x; j < p.V; j += kThreads) {
-    const uint64_t k = order_key(to_f32(x[j]), j);
-    best = k > best ? k : best;
-  }
-  best = block_max_key(best);
-  const float m = to_f32(x[~static_cast<uint32_t>(best)]);
-  float s = 0.0f, t = 0.0f;
-  if (m != -INFINITY) {
-    for (int j = threadIdx.x; j < p.V; j += kThreads) {
-      const float d = to_f32(x[j]) - m, e = expf(d);
-      s += e;
-      t += e == 0.0f ? 0.0f : e * d;
+  const E* x = static_cast<const E*>(p.logits) + i * p.ld;
+  const int vecs = (p.V + VEC - 1) / VEC, per = (vecs + ranks - 1) / ranks;
+  const int v0 = min(rank * per, vecs), v1 = min(v0 + per, vecs);
+
+  Sums a = {-INFINITY, 0.0f, 0.0f};
+  auto take = [&](const uint4& q) {
+    float2 f[8 / sizeof(E)];
+    pairs<E>(q, f);
+    const float base = a.m == -INFINITY ? 0.0f : a.m;
+    float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      float2 d = fmul2(fadd2(f[e], make_float2(-base, -base)), make_float2(kLog2e, kLog2e));
+      // 2^-200 is 0 in fp32: the clamp only keeps 0 * -inf out of t
+      d.x = max_nan(d.x, -200.0f);
+      d.y = max_nan(d.y, -200.0f);
+      const float2 g = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+      s2 = fadd2(s2, g);
+      t2 = ffma2(g, d, t2);
     }
-    s = block_sum(s);
-    t = block_sum(t);
+    a.s += s2.x + s2.y;
+    a.t += t2.x + t2.y;
+  };
+  int v = v0 + tid;
+  for (; v + (U - 1) * NT < v1 && (v + (U - 1) * NT + 1) * VEC <= p.V; v += U * NT) {
+    uint4 q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
+    float big = largest<E>(q[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) big = max_nan(big, largest<E>(q[u]));
+    if (!(big <= a.m)) a.raise(max_nan(a.m, big));
+#pragma unroll
+    for (int u = 0; u < U; ++u) take(q[u]);
   }
-  const float lse = s == 0.0f ? -INFINITY : m + logf(s);
-  if (threadIdx.x == 0) {
+  for (; v < v1; v += NT) {
+    const uint4 q = load_vec<E>(x, v, p.V);
+    const float big = largest<E>(q);
+    if (!(big <= a.m)) a.raise(max_nan(a.m, big));
+    take(q);
+  }
+  if (p.top > 0) sh.key[tid] = v0 + tid < v1 ? value_key(a.m) : 0u;
+  if (tid == 0) {
+    sh.owners = 0;
+    sh.found = 0;
+  }
+
+  // ---- the row's sums
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Sums b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+    a.add(b);
+  }
+  if (lane == 0) sh.warp[w] = a;
+  __syncthreads();
+  if (w == 0) {
+    a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Sums b;
+      b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+      b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+      b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+      a.add(b);
+    }
+    if (lane == 0) sh.part = a;
+    if (p.top > 0) {
+      // the top-th largest of the threads' keys, bit by bit: bf16 keys differ in their upper 16 bits only
+      uint32_t k[NT / 32], bound = 0;
+#pragma unroll
+      for (int e = 0; e < NT / 32; ++e) k[e] = sh.key[lane + 32 * e];
+      for (int bit = 31; bit >= (sizeof(E) == 4 ? 0 : 16); --bit) {
+        const uint32_t t = bound | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < NT / 32; ++e) c += k[e] >= t;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (c >= p.top) bound = t;
+        if (c == p.top) break;
+      }
+      if (lane == 0) sh.bound = bound;
+    }
+  }
+  int local = 0;  // alternatives this block has: min(top, its elements)
+  if (p.top > 0) {
+    const int64_t first = static_cast<int64_t>(v0) * VEC, last = min(static_cast<int64_t>(v1) * VEC, static_cast<int64_t>(p.V));
+    local = static_cast<int>(min(static_cast<int64_t>(p.top), max(last - first, static_cast<int64_t>(0))));
+    __syncthreads();
+    const uint32_t bound = sh.bound;
+    if (v0 + tid < v1 && sh.key[tid] >= bound) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
+    __syncthreads();
+    for (int o = w; o < sh.owners; o += NT / 32) {
+      for (int u = v0 + sh.owner[o] + lane * NT; u < v1; u += 32 * NT) {
+        const uint4 q = load_vec<E>(x, u, p.V);
+        const E* e = reinterpret_cast<const E*>(&q);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const uint32_t j = u * VEC + k, key = value_key(to_f32(e[k]));
+          if (key >= bound && j < static_cast<uint32_t>(p.V)) {
+            const int at = atomicAdd(&sh.found, 1);
+            if (at < kCandidates) sh.cand[at] = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(~j);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.found;
+    if (n <= kCandidates) {
+      for (int c = tid; c < n; c += NT) {
+        const uint64_t mine = sh.cand[c];
+        int before = 0;
+        for (int o = 0; o < n; ++o) before += sh.cand[o] > mine;
+        if (before < local) sh.best[before] = mine;
+      }
+    } else {
+      uint64_t below = ~0ull;
+      for (int k = 0; k < local; ++k) {
+        uint64_t best = 0;
+        for (int u = v0 + tid; u < v1; u += NT) {
+          const uint4 q = load_vec<E>(x, u, p.V);
+          const E* e = reinterpret_cast<const E*>(&q);
+#pragma unroll
+          for (int z = 0; z < VEC; ++z) {
+            const uint32_t j = u * VEC + z;
+            const uint64_t key = (static_cast<uint64_t>(value_key(to_f32(e[z]))) << 32) | static_cast<uint32_t>(~j);
+            if (j < static_cast<uint32_t>(p.V) && key < below && key > best) best = key;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t b = __shfl_xor_sync(0xffffffffu, best, o);
+          best = b > best ? b : best;
+        }
+        if (lane == 0) sh.red[w] = best;
+        __syncthreads();
+        for (int o = 0; o < NT / 32; ++o) best = sh.red[o] > best ? sh.red[o] : best;
+        if (tid == 0) sh.best[k] = best;
+        below = best;
+        __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the cluster's parts, collected by its first block
+  Sums row = sh.part;
+  if constexpr (CLUSTER) {
+    cluster_sync();
+    if (rank == 0) {
+      for (int r = 1; r < ranks; ++r) {
+        const uint32_t at = mapa_shared(smem_u32(&sh.part), r);
+        Sums b;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + 4) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.t) : "r"(at + 8) : "memory");
+        row.add(b);
+      }
+      // every block's alternatives side by side; a block with fewer has the key 0 in their place
+      static_assert(kMaxCluster * kMaxTop <= kCandidates, "the cluster's alternatives fit the candidates");
+      for (int c = tid; c < ranks * p.top; c += NT) {
+        const int r = c / p.top, k = c % p.top;
+        const int r0 = min(r * per, vecs), r1 = min(r0 + per, vecs);
+        const int64_t have = min(static_cast<int64_t>(r1) * VEC, static_cast<int64_t>(p.V)) - static_cast<int64_t>(r0) * VEC;
+        uint64_t key = 0;
+        if (k < have) {
+          const uint32_t at = mapa_shared(smem_u32(&sh.best[k]), r);
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(at) : "memory");
+        }
+        sh.cand[c] = key;
+      }
+    }
+    cluster_sync();  // the other blocks' shared memory was read
+    if (rank != 0) return;
+    if (p.top > 0) {
+      __syncthreads();
+      const int n = ranks * p.top;
+      uint64_t keep[kMaxCluster * kMaxTop / NT + 1];
+      int before[kMaxCluster * kMaxTop / NT + 1];
+#pragma unroll
+      for (int e = 0; e < kMaxCluster * kMaxTop / NT + 1; ++e) {
+        const int c = tid + e * NT;
+        before[e] = p.top;
+        if (c < n) {
+          keep[e] = sh.cand[c];
+          before[e] = 0;
+          for (int o = 0; o < n; ++o) before[e] += sh.cand[o] > keep[e];
+          if (keep[e] == 0) before[e] = p.top;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kMaxCluster * kMaxTop / NT + 1; ++e)
+        if (before[e] < p.top) sh.best[before[e]] = keep[e];
+      __syncthreads();
+    }
+  }
+
+  // ---- results
+  const bool empty = row.s == 0.0f;  // nothing but -inf
+  const float log_s = logf(row.s);
+  if (tid == 0) {
     const int tgt = p.targets[i];
     float lp = 0.0f;
     if (tgt >= p.V)
       atomicOr(&g_logprobs_status, kDevBadIndex);
     else if (tgt >= 0)
-      lp = s == 0.0f ? -INFINITY : (to_f32(x[tgt]) - m) - logf(s);
+      lp = empty ? -INFINITY : (to_f32(x[tgt]) - row.m) - log_s;
     p.logp[i] = lp;
-    if (p.entropy) p.entropy[i] = s == 0.0f ? 0.0f : logf(s) - t / s;
-    if (p.lse) p.lse[i] = lse;
+    if (p.entropy) p.entropy[i] = empty ? 0.0f : log_s - row.t / row.s * kLn2;
+    if (p.lse) p.lse[i] = empty ? -INFINITY : row.m + log_s;
   }
-  for (int k = 0; k < p.top; ++k) {
-    if (threadIdx.x == 0) {
-      const uint32_t j = ~static_cast<uint32_t>(best);
-      p.top_ids[i * p.top + k] = static_cast<int>(j);
-      p.top_logp[i * p.top + k] = s == 0.0f ? -INFINITY : (to_f32(x[j]) - m) - logf(s);
-    }
-    uint64_t next = 0;
-    for (int j = threadIdx.x; j < p.V; j += kThreads) {
-      const uint64_t key = order_key(to_f32(x[j]), j);
-      next = key < best && key > next ? key : next;
-    }
-    best = block_max_key(next);
+  for (int k = tid; k < p.top; k += NT) {
+    const uint64_t key = sh.best[k];
+    p.top_ids[i * p.top + k] = static_cast<int>(~static_cast<uint32_t>(key));
+    p.top_logp[i * p.top + k] = empty ? -INFINITY : (key_value(static_cast<uint32_t>(key >> 32)) - row.m) - log_s;
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const __grid_constant__ LogprobsGradParams p) {
+// Gradient: element by element, bound by reading the logits and writing the
+// gradient.  A block takes kGradVecs vectors a thread of one row, so the row's
+// statistics are read once for 16 KB and the loads are in flight meanwhile.
+//   dx = 2^(lp log2 e) (A + B lp),  lp = x - lse, A = -(dlogp + dH H), B = -dH
+constexpr int kGradThreads = 256, kGradVecs = 4;
+
+template <class E>
+__global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const __grid_constant__ LogprobsGradParams p) {
+  constexpr int VEC = 16 / sizeof(E);
+  const int64_t i = blockIdx.x / p.blocks;
+  const int v0 = static_cast<int>(blockIdx.x % p.blocks) * kGradThreads * kGradVecs + threadIdx.x;
+  const E* x = static_cast<const E*>(p.logits) + i * p.ld;
+  E* dx = static_cast<E*>(p.dlogits) + i * p.ldd;
+  const int vecs = (p.V + VEC - 1) / VEC;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i = blockIdx.x;
-  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
-  T* dx = static_cast<T*>(p.dlogits) + i * p.ldd;
+  uint4 q[kGradVecs];
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u)
+    if (v0 + u * kGradThreads < vecs) q[u] = load_vec<E>(x, v0 + u * kGradThreads, p.V);
   int tgt = p.targets[i];
   if (tgt >= p.V) {
-    if (threadIdx.x == 0) atomicOr(&g_logprobs_status, kDevBadIndex);
+    if (v0 == 0) atomicOr(&g_logprobs_status, kDevBadIndex);
     tgt = -1;
   }
   const float lse = p.lse[i], H = p.entropy ? p.entropy[i] : 0.0f;
-  const float dl = p.dlogp && tgt >= 0 ? p.dlogp[i] : 0.0f, dh = p.dentropy ? p.dentropy[i] : 0.0f;
-  for (int j = threadIdx.x; j < p.V; j += kThreads) {
-    const float lp = to_f32(x[j]) - lse, e = lse == -INFINITY ? 0.0f : expf(lp);
-    float g = e == 0.0f ? 0.0f : -e * (dl + dh * (lp + H));
-    if (j == tgt) g += dl;
-    if (lse == -INFINITY) g = 0.0f;
-    if constexpr (sizeof(T) == 4)
-      dx[j] = g;
-    else
-      dx[j] = __float2bfloat16_rn(g);
+  const bool empty = lse == -INFINITY;
+  const float dl = p.dlogp && tgt >= 0 && !empty ? p.dlogp[i] : 0.0f, dh = p.dentropy && !empty ? p.dentropy[i] : 0.0f;
+  const float A = -(dl + dh * H), B = -dh;
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    const int v = v0 + u * kGradThreads;
+    if (v >= vecs) break;
+    float2 f[8 / sizeof(E)];
+    pairs<E>(q[u], f);
+    float g[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 lp = fadd2(f[e], make_float2(-lse, -lse));
+      float2 pr;
+      if constexpr (sizeof(E) == 4) {
+        pr = make_float2(expf(lp.x), expf(lp.y));
+      } else {
+        const float2 d = fmul2(lp, make_float2(kLog2e, kLog2e));
+        pr = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+      }
+      const float2 r = fmul2(pr, ffma2(make_float2(B, B), lp, make_float2(A, A)));
+      // no probability, no gradient: x = -inf would give 0 * inf, and so would an empty row
+      g[2 * e] = pr.x == 0.0f || empty ? 0.0f : r.x;
+      g[2 * e + 1] = pr.y == 0.0f || empty ? 0.0f : r.y;
+    }
+    const int at = tgt - v * VEC;
+    if (at >= 0 && at < VEC) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e == at) g[e] += dl;
+    }
+    uint4 o;
+    E* oe = reinterpret_cast<E*>(&o);
+    if constexpr (sizeof(E) == 4) {
+      o = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
+    } else {
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(g[2 * e], g[2 * e + 1]);
+    }
+    if ((v + 1) * VEC <= p.V) {
+      __stcs(reinterpret_cast<uint4*>(dx) + v, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (v * VEC + e < p.V) dx[v * VEC + e] = oe[e];
+    }
   }
+}
+
+template <class E, int NT>
+cudaError_t run_logprobs(LogprobsParams p, int64_t M, cudaStream_t s, bool pdl) {
+  // few rows: up to 8 blocks (a cluster) share a row, as long as the rows leave SMs idle and each block has at least
+  // one round of loads
+  constexpr int VEC = 16 / sizeof(E);
+  int c = 1;
+  while (c < kMaxCluster && M * c * 2 <= device_sm_count() && p.V / (c * 2) >= NT * VEC) c *= 2;
+  p.ranks = c;
+  void* args[] = {&p};
+  const void* k = c > 1 ? reinterpret_cast<const void*>(logprobs_kernel<E, NT, true>)
+                        : reinterpret_cast<const void*>(logprobs_kernel<E, NT, false>);
+  return launch_ex(k, dim3(static_cast<unsigned>(M * c)), dim3(NT), 0, s, pdl, args, c);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobsParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl) {
-  const void* k = f32 ? reinterpret_cast<const void*>(logprobs_kernel<float>)
-                      : reinterpret_cast<const void*>(logprobs_kernel<__nv_bfloat16>);
-  void* args[] = {const_cast<LogprobsParams*>(&p)};
-  return launch_ex(k, dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, s, pdl, args);
+  // short rows take small blocks
+  if (p.V <= 8192) return f32 ? run_logprobs<float, 128>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, 128>(p, M, s, pdl);
+  return f32 ? run_logprobs<float, 512>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, 512>(p, M, s, pdl);
 }
 
-cudaError_t launch_logprobs_backward(const LogprobsGradParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl) {
+int64_t logprobs_backward_blocks(int64_t V, bool f32) {
+  const int64_t per = static_cast<int64_t>(kGradThreads) * kGradVecs * (f32 ? 4 : 8);
+  return (V + per - 1) / per;
+}
+
+cudaError_t launch_logprobs_backward(const LogprobsGradParams& q, int64_t M, bool f32, cudaStream_t s, bool pdl) {
+  LogprobsGradParams p = q;
+  p.blocks = static_cast<int>(logprobs_backward_blocks(p.V, f32));
   const void* k = f32 ? reinterpret_cast<const void*>(logprobs_backward_kernel<float>)
                       : reinterpret_cast<const void*>(logprobs_backward_kernel<__nv_bfloat16>);
-  void* args[] = {const_cast<LogprobsGradParams*>(&p)};
-  return launch_ex(k, dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, s, pdl, args);
+  void* args[] = {&p};
+  return launch_ex(k, dim3(static_cast<unsigned>(M * p.blocks)), dim3(kGradThreads), 0, s, pdl, args);
 }
 
 unsigned read_clear_status_logprobs() {
