@@ -22,6 +22,7 @@ epilogue"):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -102,6 +103,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libcoda_gb300.so (compiling it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build_if_missing else _build.LIB
@@ -652,16 +655,52 @@ def coda_block_rowscale_fp8(A, amax_a, W1t, scale_w1, R, W2t, scale_w2, eps: flo
     return {"Aq": Aq, "scale_a": scale_a, "h": H, "P": P, "amax_h": amax_h, "Hq": Hq, "scale_h": scale_h, "Z": Z}
 
 
-_I32 = (torch.int32,)
+# The decode and scoring calls are short on the GPU (a few microseconds), so their argument checks are made in one
+# pass that reads each tensor's properties once; only a call that it does not pass goes through _want and _dev, which
+# say what is wrong.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _pointers(specs):
+    """Device pointers of (tensor or None, name, shape or None for one or more elements, dtype): contiguous CUDA tensors
+    on the current device, checked as by _want and _dev."""
+    try:
+        dev, out = torch.cuda.current_device() if specs[0][0].is_cuda else -2, []
+        for t, _, shape, dtype in specs:
+            if t is None:
+                out.append(None)
+            elif (t.dtype is dtype and (t.shape == shape if shape is not None else t.numel() > 0)
+                  and t.get_device() == dev and t.is_contiguous()):
+                out.append(t.data_ptr() or None)
+            else:
+                break
+        else:
+            return out
+    except AttributeError:
+        pass
+    for t, name, shape, dtype in specs:
+        _want(t, name, shape, None if dtype is None else (dtype,), numel=None if shape is not None else 1)
+    return [_dev(t, name) for t, name, _, _ in specs]
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """_stream without building a stream object for the current one."""
+    return _raw_stream(t.get_device()) if stream is None and _raw_stream is not None else _stream(t, stream)
 
 
 def _cache_shape(k_cache, v_cache, dtype):
     """(num_pages, kv_heads, page_size, head_dim, cache dtype code) of a pair of caches for rows of `dtype`."""
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache has {k_cache.dim()} dimensions, expected [num_pages, kv_heads, page_size, head_dim]")
-    _want(k_cache, "k_cache", dtypes=(dtype,) + (_BYTE if dtype == torch.bfloat16 else ()))
-    _want(v_cache, "v_cache", k_cache.shape, (k_cache.dtype,))
-    return (*k_cache.shape, _dtype_code(k_cache))
+    if k_cache.dtype is not dtype:
+        _want(k_cache, "k_cache", dtypes=(dtype,) + (_BYTE if dtype == torch.bfloat16 else ()))
+    return (*k_cache.shape, CODA_E4M3 if k_cache.dtype is not dtype else _dtype_code(k_cache))
+
+
+def _table_shape(page_table):
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has {page_table.dim()} dimensions, expected [num_seqs, max_pages]")
+    return page_table.shape
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -670,16 +709,14 @@ def _rows(t: torch.Tensor, name: str):
     apart than they are wide."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if t.is_contiguous():
-        return _dev(t, name), t[0].numel() if t.shape[0] else t.numel()
-    inner = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != inner:
-            raise ValueError(f"{name}'s rows must be contiguous")
-        inner *= n
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
-    return t.data_ptr() or None, t.stride(0) if t.shape[0] > 1 else inner
+    shape, stride, inner = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and stride[i] != inner:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        inner *= shape[i]
+    return t.data_ptr() or None, stride[0] if shape[0] > 1 else inner
 
 
 def coda_paged_append(Z, positions, page_table, k_cache, v_cache, q_heads: int, *, row_seq=None, base: float = 0.0,
@@ -690,28 +727,23 @@ def coda_paged_append(Z, positions, page_table, k_cache, v_cache, q_heads: int, 
     already rotated.  Rows with a negative position are left out.  Returns the rotated queries [M, q_heads, head_dim],
     or None with ``want_q=False``."""
     lib = load_library()
-    M = Z.shape[0]
+    M, dt = Z.shape[0], Z.dtype
     code = _dtype_code(Z)
-    pages, kv_heads, page_size, D, ccode = _cache_shape(k_cache, v_cache, Z.dtype)
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table has {page_table.dim()} dimensions, expected [num_seqs, max_pages]")
-    _want(Z, "Z", (M, (q_heads + 2 * kv_heads) * D), (torch.float32, torch.bfloat16))
-    _want(positions, "positions", (M,), _I32)
-    _want(page_table, "page_table", dtypes=_I32)
-    _want(row_seq, "row_seq", (M,), _I32)
-    _want_scalars(scale_k=scale_k, scale_v=scale_v)
+    pages, kv_heads, page_size, D, ccode = _cache_shape(k_cache, v_cache, dt)
+    seqs, max_pages = _table_shape(page_table)
     if Q is None and want_q:
-        Q = torch.empty(M, q_heads, D, dtype=Z.dtype, device=Z.device)
-    if Q is not None:
-        _want(Q, "Q", (M, q_heads, D), (Z.dtype,))
-    _check(lib.coda_paged_append(_dev(Z, "Z"), _dev(positions, "positions"), _dev(row_seq, "row_seq"),
-                                 _dev(page_table, "page_table"), _dev(Q, "Q"), _dev(k_cache, "k_cache"),
-                                 _dev(v_cache, "v_cache"), M, page_table.shape[0], page_table.shape[1], q_heads,
-                                 kv_heads, D, pages, page_size, float(base), code, ccode, _dev(scale_k, "scale_k"),
-                                 _dev(scale_v, "scale_v"), _stream(Z, stream)))
+        Q = torch.empty(M, q_heads, D, dtype=dt, device=Z.device)
+    ptr = _pointers(((Z, "Z", (M, (q_heads + 2 * kv_heads) * D), dt), (positions, "positions", (M,), torch.int32),
+                     (row_seq, "row_seq", (M,), torch.int32), (page_table, "page_table", page_table.shape, torch.int32),
+                     (Q, "Q", (M, q_heads, D), dt), (k_cache, "k_cache", k_cache.shape, k_cache.dtype),
+                     (v_cache, "v_cache", k_cache.shape, k_cache.dtype), (scale_k, "scale_k", None, torch.float32),
+                     (scale_v, "scale_v", None, torch.float32)))
+    _check(lib.coda_paged_append(*ptr[:7], M, seqs, max_pages, q_heads, kv_heads, D, pages, page_size, base, code, ccode,
+                                 ptr[7], ptr[8], _stream_of(Z, stream)))
     return Q
 
 
+@functools.lru_cache(maxsize=None)
 def coda_paged_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(load_library().coda_paged_attention_workspace_bytes(q_heads, kv_heads, head_dim))
 
@@ -734,29 +766,24 @@ def coda_paged_attention(Q, k_cache, v_cache, page_table, lengths, workspace, *,
     if Q.dim() != 3:
         raise ValueError(f"Q has {Q.dim()} dimensions, expected [M, q_heads, head_dim]")
     M, q_heads, D = Q.shape
-    code = _dtype_code(Q)
-    pages, kv_heads, page_size, Dk, ccode = _cache_shape(k_cache, v_cache, Q.dtype)
+    dt, code = Q.dtype, _dtype_code(Q)
+    pages, kv_heads, page_size, Dk, ccode = _cache_shape(k_cache, v_cache, dt)
     if Dk != D:
         raise ValueError(f"Q has head_dim {D}, the caches {Dk}")
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table has {page_table.dim()} dimensions, expected [num_seqs, max_pages]")
-    _want(page_table, "page_table", dtypes=_I32)
-    _want(lengths, "lengths", (M,), _I32)
-    _want(row_seq, "row_seq", (M,), _I32)
-    _want(lse, "lse", (M, q_heads), _F32)
-    _want_scalars(scale_k=scale_k, scale_v=scale_v)
-    _want(workspace, "workspace", nbytes=lib.coda_paged_attention_workspace_bytes(q_heads, kv_heads, D))
+    seqs, max_pages = _table_shape(page_table)
+    _want(workspace, "workspace", nbytes=coda_paged_attention_workspace_bytes(q_heads, kv_heads, D))
     if O is None:
-        O = torch.empty(M, q_heads * D, dtype=Q.dtype, device=Q.device)
-    _want(O, "O", (M, q_heads * D), (Q.dtype,))
+        O = torch.empty(M, q_heads * D, dtype=dt, device=Q.device)
+    ptr = _pointers(((O, "O", (M, q_heads * D), dt), (k_cache, "k_cache", k_cache.shape, k_cache.dtype),
+                     (v_cache, "v_cache", k_cache.shape, k_cache.dtype),
+                     (page_table, "page_table", page_table.shape, torch.int32), (lengths, "lengths", (M,), torch.int32),
+                     (row_seq, "row_seq", (M,), torch.int32), (lse, "lse", (M, q_heads), torch.float32),
+                     (scale_k, "scale_k", None, torch.float32), (scale_v, "scale_v", None, torch.float32),
+                     (workspace, "workspace", workspace.shape, workspace.dtype)))
     q_ptr, ldq = _rows(Q, "Q")
-    _check(lib.coda_paged_attention(q_ptr, max(ldq, q_heads * D), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-                                    _dev(page_table, "page_table"), _dev(lengths, "lengths"),
-                                    _dev(row_seq, "row_seq"), _dev(O, "O"), _dev(lse, "lse"), M, page_table.shape[0],
-                                    page_table.shape[1], q_heads, kv_heads, D, pages, page_size,
-                                    D ** -0.5 if scale is None else float(scale), code, ccode,
-                                    _dev(scale_k, "scale_k"), _dev(scale_v, "scale_v"),
-                                    _dev(workspace, "workspace"), _stream(Q, stream)))
+    _check(lib.coda_paged_attention(q_ptr, ldq, *ptr[1:6], ptr[0], ptr[6], M, seqs, max_pages, q_heads, kv_heads, D,
+                                    pages, page_size, D ** -0.5 if scale is None else scale, code, ccode, ptr[7],
+                                    ptr[8], ptr[9], _stream_of(Q, stream)))
     return O
 
 
@@ -779,22 +806,19 @@ def coda_logprobs(logits, targets, top: int = 0, *, logp=None, entropy=None, lse
         raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
     M, V = logits.shape
     _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
-    _want(targets, "targets", (M,), _I32)
-    e = lambda *shape, dt=torch.float32: torch.empty(*shape, dtype=dt, device=logits.device)  # noqa: E731
+    f32, e = torch.float32, lambda *shape, dt=torch.float32: torch.empty(*shape, dtype=dt, device=logits.device)
     out = {"logp": e(M) if logp is None else logp, "entropy": e(M) if entropy is None else entropy,
            "lse": e(M) if lse is None else lse}
     if top > 0:
-        out["top_logp"] = e(M, top) if top_logp is None else top_logp
-        out["top_ids"] = e(M, top, dt=torch.int32) if top_ids is None else top_ids
-        _want(out["top_logp"], "top_logp", (M, top), _F32)
-        _want(out["top_ids"], "top_ids", (M, top), _I32)
-    for k in ("logp", "entropy", "lse"):
-        _want(out[k], k, (M,), _F32)
-    ptr, ld = _logits_rows(logits, "logits")
-    _check(lib.coda_logprobs(ptr, ld, _dev(targets, "targets"), _dev(out["logp"], "logp"),
-                             _dev(out["entropy"], "entropy"), _dev(out["lse"], "lse"),
-                             _dev(out.get("top_logp"), "top_logp"), _dev(out.get("top_ids"), "top_ids"), M, V, top,
-                             _dtype_code(logits), _stream(logits, stream)))
+        top_logp = out["top_logp"] = e(M, top) if top_logp is None else top_logp
+        top_ids = out["top_ids"] = e(M, top, dt=torch.int32) if top_ids is None else top_ids
+    else:
+        top_logp = top_ids = None
+    ptr = _pointers(((targets, "targets", (M,), torch.int32), (out["logp"], "logp", (M,), f32),
+                     (out["entropy"], "entropy", (M,), f32), (out["lse"], "lse", (M,), f32),
+                     (top_logp, "top_logp", (M, top), f32), (top_ids, "top_ids", (M, top), torch.int32)))
+    row, ld = _logits_rows(logits, "logits")
+    _check(lib.coda_logprobs(row, ld, *ptr, M, V, top, _dtype_code(logits), _stream_of(logits, stream)))
     return out
 
 
@@ -805,19 +829,17 @@ def coda_logprobs_backward(logits, targets, lse, entropy=None, dlogp=None, dentr
     if logits.dim() != 2:
         raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
     M, V = logits.shape
-    _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
-    _want(targets, "targets", (M,), _I32)
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
-        _want(t, name, (M,), _F32)
+    f32 = torch.float32
+    _want(logits, "logits", dtypes=(f32, torch.bfloat16))
     if dlogits is None:  # rows on 16-byte boundaries, as the logits' own
         step = 16 // logits.element_size()
         dlogits = torch.empty(M, -(-V // step) * step, dtype=logits.dtype, device=logits.device)[:, :V]
     _want(dlogits, "dlogits", (M, V), (logits.dtype,))
-    ptr, ld = _logits_rows(logits, "logits")
-    dptr, ldd = _logits_rows(dlogits, "dlogits")
-    _check(lib.coda_logprobs_backward(ptr, ld, _dev(targets, "targets"), _dev(lse, "lse"), _dev(entropy, "entropy"),
-                                      _dev(dlogp, "dlogp"), _dev(dentropy, "dentropy"), dptr, ldd, M, V,
-                                      _dtype_code(logits), _stream(logits, stream)))
+    ptr = _pointers(((targets, "targets", (M,), torch.int32), (lse, "lse", (M,), f32), (entropy, "entropy", (M,), f32),
+                     (dlogp, "dlogp", (M,), f32), (dentropy, "dentropy", (M,), f32)))
+    row, ld = _logits_rows(logits, "logits")
+    drow, ldd = _logits_rows(dlogits, "dlogits")
+    _check(lib.coda_logprobs_backward(row, ld, *ptr, drow, ldd, M, V, _dtype_code(logits), _stream_of(logits, stream)))
     return dlogits
 
 
