@@ -1070,7 +1070,8 @@ coda_status check_paged(int64_t M, int64_t num_seqs, int64_t max_pages, int64_t 
   REQUIRE(head_dim > 0 && head_dim <= coda::kMaxHeadDim && head_dim % step == 0,
           "head_dim = %" PRId64 " must be a multiple of %" PRId64 " for this cache, at most %d", head_dim, step,
           coda::kMaxHeadDim);
-  REQUIRE(num_pages < (int64_t(1) << 60) / page_size / kv_heads / head_dim, "a cache of 2^60 elements or more");
+  REQUIRE(num_pages < INT32_MAX / page_size / kv_heads,
+          "num_pages * kv_heads * page_size: a cache of 2^31 rows or more");
   REQUIRE(M < (int64_t(1) << 60) / (q_heads + 2 * kv_heads) / head_dim, "rows of 2^60 elements or more");
   REQUIRE(num_seqs * max_pages < (int64_t(1) << 60), "a page table of 2^60 entries or more");
   if (cache_dtype == CODA_E4M3) {

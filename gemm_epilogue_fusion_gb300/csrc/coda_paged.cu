@@ -188,26 +188,36 @@ constexpr int kMaxWorkers = 512;  // blocks of a grid: bounds the workspace
 constexpr int kMinTiles = 2;      // tiles a block takes at least
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <class T, class C, int DP_, bool WIDE_>
+
+// What a block does with a key/value head's query heads at a time:
+//   kFew   up to 4 (fp32: 1);  kSome  up to 8;  kMany  up to 16 (fp32: 8)
+enum Heads { kFew, kSome, kMany };
+
+template <class T, class C, int DP_, Heads HEADS_>
 struct AttnShape {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr bool E4M3 = sizeof(C) == 1;
-  static constexpr bool WIDE = WIDE_;  // more than 8 (fp32: more than 1) query heads of a key/value head at a time
-  static constexpr int DP = DP_;       // head_dim rounded up
-  static constexpr int RG = F32 ? (WIDE ? 8 : 1) : (WIDE ? 16 : 8);  // query heads of a block
-  static constexpr int PITCH = DP * static_cast<int>(sizeof(C));     // bytes of a staged row
-  static constexpr int KT0 = 4096 / PITCH, KMIN = F32 ? 8 : 16;
-  static constexpr int KT = F32 ? (DP == 256 ? 8 : 16) : (KT0 < KMIN ? KMIN : KT0);  // keys of a warp's tile
+  static constexpr Heads HEADS = HEADS_;
+  static constexpr int DP = DP_;                              // head_dim rounded up
+  static constexpr int NH = HEADS == kMany ? 2 : 1;           // mma: tiles of 8 heads
+  static constexpr int RG = F32 ? (HEADS == kFew ? 1 : 8) : 8 * NH;   // rows of state
+  static constexpr int MAXG = F32 ? RG : HEADS == kFew ? 4 : RG;      // query heads of a block
+  static constexpr int PITCH = DP * static_cast<int>(sizeof(C));      // bytes of a staged row
+  static constexpr int KT0 = 4096 / PITCH;
+  static constexpr int KT = F32 ? (DP == 256 ? 8 : 16) : KT0 < 16 ? 16 : KT0 > 32 ? 32 : KT0;  // keys of a warp's tile
   static constexpr int CT = KT * kAttnWarps;
-  static constexpr int ST = 3;
-  static constexpr int KPL = (KT + 31) / 32;  // keys per lane when pages are looked up
+  static constexpr int ST = 2;
   static constexpr int STAGE = 2 * KT * PITCH;
   static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
   static constexpr int RING = kAttnWarps * ST * STAGE;
-  static constexpr int JOIN = 2 * RG * DP * 4;
+  static constexpr int OS = DP + 4;  // floats between the rows of a join buffer
+  static constexpr int JOIN = 2 * RG * OS * 4;
   static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : 0;
   static constexpr int SMEM = RING + JOIN + QBYTES;
-  static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;
+  static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + DP / 8) + 72;  // about what a thread needs
+  static constexpr int BY_SMEM = 233472 / (SMEM + 1024 + 640), BY_REGS = 65536 / (kAttnThreads * REGS);
+  static constexpr int CTAS0 = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
+  static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > 3 ? 3 : CTAS0;  // blocks on an SM
 };
 
 // Chunk c of staged row `row`: 16-byte chunks are permuted within 128 bytes so
@@ -252,6 +262,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
   uint32_t d;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(codes));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t codes) {  // ... of the high 16 bits
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(codes));
+  return d;
+}
+// An 8 x 8 matrix of 16-bit values, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 template <bool F16>
@@ -304,20 +325,20 @@ struct Cursor {
   }
 };
 
-template <class E, class C, int DP, bool WIDE>
-__global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
+template <class E, class C, int DP, Heads HEADS>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
-  using S = AttnShape<E, C, DP, WIDE>;
-  constexpr int KT = S::KT, CT = S::CT, ST = S::ST, PITCH = S::PITCH, CPR = S::CPR, KPL = S::KPL, RG = S::RG;
+  using S = AttnShape<E, C, DP, HEADS>;
+  constexpr int KT = S::KT, CT = S::CT, ST = S::ST, PITCH = S::PITCH, CPR = S::CPR, RG = S::RG, NH = S::NH, OS = S::OS;
   constexpr bool F16 = S::E4M3;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kAttnWarps];
   __shared__ int s_start[3], s_last;
-  __shared__ uint32_t s_mask[kAttnWarps][ST][2];
+  __shared__ uint32_t s_mask[kAttnWarps][ST];
   __shared__ float s_ml[2][RG][2];
-  float* s_o = reinterpret_cast<float*>(smem + S::RING);  // [2][RG][DP]
+  float* s_o = reinterpret_cast<float*>(smem + S::RING);  // [2][RG][OS]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int G = p.q_heads / p.kv_heads, groups = (G + RG - 1) / RG, gsize = (G + groups - 1) / groups;
+  const int G = p.q_heads / p.kv_heads, groups = (G + S::MAXG - 1) / S::MAXG, gsize = (G + groups - 1) / groups;
   const int units = p.kv_heads * groups;
   const int chunks = p.head_dim * static_cast<int>(sizeof(C)) / 16;
   const uint32_t ring = smem_u32(smem) + w * ST * S::STAGE;
@@ -381,52 +402,42 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
   in.t = s_start[2];
   in.enter(p, CT);
   Cursor at = in;
-  int pg[KPL], slot[KPL];
+  int pg, slot;
   bool bad_page = false;
   auto look_up = [&]() {
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-      const int key = in.t * CT + w * KT + lane + 32 * j;
-      pg[j] = -1;
-      slot[j] = -1;  // no such key
-      if (lane + 32 * j < KT && key < in.len) {
-        const int q = key / p.page_size;
-        slot[j] = key - q * p.page_size;
-        pg[j] = __ldg(p.page_table + static_cast<int64_t>(in.seq) * p.max_pages + q);
-      }
+    const int key = in.t * CT + w * KT + lane;
+    pg = -1;
+    slot = -1;  // no such key
+    if (lane < KT && key < in.len) {
+      const int q = key / p.page_size;
+      slot = key - q * p.page_size;
+      pg = __ldg(p.page_table + static_cast<int64_t>(in.seq) * p.max_pages + q);
     }
   };
+  const int row_bytes = p.head_dim * static_cast<int>(sizeof(C));
+  constexpr int LPR = CPR < 32 ? CPR : 32;  // lanes of a row
+  const char* const k_src = static_cast<const char*>(p.Kc) + (lane % LPR) * 16;
+  const char* const v_src = static_cast<const char*>(p.Vc) + (lane % LPR) * 16;
   auto issue = [&](int stage) {
-    const int hk = in.h / groups;
-    int64_t off[KPL];
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-      const bool ok = pg[j] >= 0 && pg[j] < p.num_pages && slot[j] >= 0;
-      bad_page |= !ok && slot[j] >= 0;
-      off[j] = ok ? ((static_cast<int64_t>(pg[j]) * p.kv_heads + hk) * p.page_size + slot[j]) * p.head_dim *
-                        static_cast<int64_t>(sizeof(C))
-                  : -1;
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) s_mask[w][stage][j] = mask;
-    }
+    const bool ok = pg >= 0 && pg < p.num_pages && slot >= 0;
+    bad_page |= !ok && slot >= 0;
+    // row of the caches (fewer than 2^31); -1: filled with zeros
+    const int mine = ok ? (pg * p.kv_heads + in.h / groups) * p.page_size + slot : -1;
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) s_mask[w][stage] = mask;
     const uint32_t dst = ring + stage * S::STAGE;
-    constexpr int LPR = CPR < 32 ? CPR : 32;  // lanes of a row
 #pragma unroll
     for (int r0 = 0; r0 < KT; r0 += 32 / LPR) {
       const int row = r0 + lane / LPR;
-      int64_t o = __shfl_sync(0xffffffffu, off[0], row & 31);
-      if constexpr (KPL == 2) {
-        const int64_t o2 = __shfl_sync(0xffffffffu, off[1], row & 31);
-        o = row < 32 ? o : o2;
-      }
+      const int from = __shfl_sync(0xffffffffu, mine, row);
+      const int64_t off = static_cast<int64_t>(max(from, 0)) * row_bytes;
 #pragma unroll
       for (int c0 = 0; c0 < CPR; c0 += LPR) {
         const int c = c0 + lane % LPR;
         if (c < chunks) {
-          const int64_t src = (o < 0 ? 0 : o) + c * 16;
           const int to = staged<PITCH>(row, c);
-          cp_async16(dst + to, static_cast<const char*>(p.Kc) + src, o >= 0);
-          cp_async16(dst + KT * PITCH + to, static_cast<const char*>(p.Vc) + src, o >= 0);
+          cp_async16(dst + to, k_src + off + c0 * 16, from >= 0);
+          cp_async16(dst + KT * PITCH + to, v_src + off + c0 * 16, from >= 0);
         }
       }
     }
@@ -442,13 +453,17 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
     cp_async_commit();
   }
 
-  // ---- per-warp state.  mma: rows lane / 4 (and, WIDE, lane / 4 + 8); fp32:
-  // columns of this lane.
-  constexpr int OW = S::F32 ? RG * DP / 32 : DP / 2;
-  constexpr int NR = S::F32 ? RG : (WIDE ? 2 : 1);
+  // ---- per-warp state.  mma: the keys (then the columns) are the 16 rows of the
+  // instruction and the heads its 8 columns, so a lane holds heads 2 (lane % 4)
+  // and the next one of each tile of 8; fp32: all heads, some columns.
+  constexpr int OW = S::F32 ? RG * DP / 32 : NH * DP / 4;
+  constexpr int NR = S::F32 ? RG : 2 * NH;
   constexpr int KS = DP / 16;
+  // kFew, bf16: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to bf16;
+  // kSome, bf16: a second product does.  f16 weights (e4m3 caches) lose 2^-11, kMany rounds once (2^-8 at most).
+  constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && !F16 && HEADS == kSome;
   float o[OW], m[NR], l[NR];
-  uint32_t q[S::F32 ? 1 : KS * (WIDE ? 4 : 2)] = {};
+  uint32_t q[S::F32 ? 1 : NH * KS * 2] = {};
   float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)
   float* s_q = reinterpret_cast<float*>(smem + S::RING + S::JOIN);  // fp32: [RG][DP]
   float* s_p = s_q + RG * DP + w * KT * RG;                         // fp32: [KT][RG] of this warp
@@ -474,11 +489,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
       }
       __syncthreads();
     } else {
-      constexpr int QR = WIDE ? 4 : 2;
       const int c4 = lane & 3;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int g = (lane >> 2) + 8 * r;
+      for (int nh = 0; nh < NH; ++nh) {
+        const int g = LOW_COLS ? (lane >> 2) & 3 : (lane >> 2) + 8 * nh;
         const uint32_t* row = reinterpret_cast<const uint32_t*>(src + static_cast<int64_t>(g) * p.head_dim);
         float big = 0.0f;
 #pragma unroll
@@ -488,7 +502,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
             // e4m3: the 16 columns of a step in the order of the staged bytes (see the products)
             const int d = ks * 16 + (S::E4M3 ? 4 * c4 + 2 * x : 2 * c4 + 8 * x);
             const uint32_t v = g < ng && d < p.head_dim ? __ldg(row + d / 2) : 0u;
-            q[ks * QR + (WIDE ? 2 * x + r : x)] = v;
+            q[(nh * KS + ks) * 2 + x] = v;
             const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
             big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
@@ -500,147 +514,159 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
           const int ex = big > 0.0f ? min(max(14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127), -112), 126) : 0;
           const float up = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
+          for (int i = 0; i < 2 * KS; ++i) {
+            uint32_t& v = q[nh * KS * 2 + i];
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+            v = pack2<true>(f.x * up, f.y * up);
+          }
+          const float down = sk * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t& v = q[ks * QR + (WIDE ? 2 * x + r : x)];
-              const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
-              v = pack2<true>(f.x * up, f.y * up);
-            }
-          s2[r] = sk * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          for (int x = 0; x < 2; ++x) s2[2 * nh + x] = __shfl_sync(0xffffffffu, down, (2 * c4 + x) * 4);
         }
       }
     }
   };
 
   // One tile of the products on the tensor cores.
-  auto tile_mma = [&](int stage) {
-    constexpr int NT = KT / 8, QR = WIDE ? 4 : 2;
+  auto tile_mma = [&](int stage, uint32_t mask) {
+    constexpr int MT = KT < 16 ? 1 : KT / 16;
     const uint32_t kb = ring + stage * S::STAGE, vb = kb + KT * PITCH;
-    float s[NT][4];
+    // s^T = k q^T: 16 keys by 8 heads a tile
+    float s[NH][MT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[t][x] = 0.0f;
-    auto a_of = [&](int ks, int x) -> uint32_t { return WIDE ? q[ks * QR + x] : (x & 1) ? 0u : q[ks * QR + x / 2]; };
-    if constexpr (!S::E4M3) {
-      // two blocks of 8 keys and 16 columns by one ldmatrix
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; t += 2)
+        for (int x = 0; x < 4; ++x) s[nh][t][x] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int row = t * 16 + (lane & 15);
+      if constexpr (!S::E4M3) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b[4];
-          ldmatrix4<false>(b, kb + staged<PITCH>(t * 8 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
-          mma16816<F16>(s[t], a_of(ks, 0), a_of(ks, 1), a_of(ks, 2), a_of(ks, 3), b[0], b[1]);
-          mma16816<F16>(s[t + 1], a_of(ks, 0), a_of(ks, 1), a_of(ks, 2), a_of(ks, 3), b[2], b[3]);
-        }
-    } else {
-      // a lane's 4 bytes are 4 consecutive columns: the pairs (0, 1) and (2, 3) are taken as the instruction's
-      // columns 2 c4 and 2 c4 + 8, for q and k alike
+          uint32_t a[4];
+          ldmatrix4<false>(a, kb + staged<PITCH>(row, ks * 2 + (lane >> 4)));
 #pragma unroll
-      for (int t = 0; t < NT; t += 2)
+          for (int nh = 0; nh < NH; ++nh)
+            mma16816<F16>(s[nh][t], a[0], a[1], a[2], a[3], q[(nh * KS + ks) * 2], q[(nh * KS + ks) * 2 + 1]);
+        }
+      } else {
+        // a lane's 4 bytes are 4 consecutive columns: the pairs (0, 1) and (2, 3) are taken as the instruction's
+        // columns 2 c4 and 2 c4 + 8, for q and k alike
 #pragma unroll
         for (int ks = 0; ks < KS; ks += 2) {
-          uint32_t b[4];
-          ldmatrix4<false>(b, kb + staged<PITCH>(t * 8 + (lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
+          uint32_t a[4];
+          ldmatrix4<false>(a, kb + staged<PITCH>(row, ks + (lane >> 4)));
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int tt = t + u / 2, kk = ks + (u & 1);
-            mma16816<F16>(s[tt], a_of(kk, 0), a_of(kk, 1), a_of(kk, 2), a_of(kk, 3), e4m3x2_f16x2(b[u]),
-                          e4m3x2_f16x2(b[u] >> 16));
-          }
-        }
-    }
-    // weights
-    const uint32_t mask0 = s_mask[w][stage][0], mask1 = KPL == 2 ? s_mask[w][stage][1] : 0u;
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t a0 = e4m3x2_f16x2(a[2 * u]), a1 = e4m3x2_f16x2(a[2 * u + 1]);
+            const uint32_t a2 = e4m3x2_f16x2_hi(a[2 * u]), a3 = e4m3x2_f16x2_hi(a[2 * u + 1]);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float big = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = t * 8 + 2 * (lane & 3) + x;
-          const bool there = ((key < 32 ? mask0 : mask1) >> (key & 31)) & 1u;
-          float& v = s[t][2 * r + x];
-          v = there ? v * s2[r] : -INFINITY;
-          big = fmaxf(big, v);
-        }
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      if (__any_sync(0xffffffffu, big > m[r])) {
-        const float mn = fmaxf(m[r], big);
-        const float c = mn == -INFINITY ? 1.0f : ex2_approx(m[r] - mn);
-        m[r] = mn;
-        l[r] *= c;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          if constexpr (WIDE) {
-            o[4 * i + 2 * r] *= c;
-            o[4 * i + 2 * r + 1] *= c;
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[4 * i + x] *= c;
+            for (int nh = 0; nh < NH; ++nh)
+              mma16816<F16>(s[nh][t], a0, a1, a2, a3, q[(nh * KS + ks + u) * 2], q[(nh * KS + ks + u) * 2 + 1]);
           }
         }
       }
+    }
+    // weights 2^(s2 s - m)
+    if (mask != (KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u)) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          if (!((mask >> (t * 16 + hf * 8 + (lane >> 2))) & 1u))
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) s[nh][t][2 * hf] = s[nh][t][2 * hf + 1] = -INFINITY;
+    }
+    float big[NR];
+    bool more = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      big[r] = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) big[r] = fmaxf(big[r], fmaxf(s[r >> 1][t][r & 1], s[r >> 1][t][2 + (r & 1)]));
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], x));
+      big[r] *= s2[r];
+      more |= big[r] > m[r];
+    }
+    if (__any_sync(0xffffffffu, more)) {
+      float c[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float mn = fmaxf(m[r], big[r]);
+        c[r] = mn == -INFINITY ? 1.0f : ex2_approx(m[r] - mn);
+        m[r] = mn;
+        l[r] *= c[r];
+      }
+#pragma unroll
+      for (int i = 0; i < OW; ++i) o[i] *= c[i / (DP / 4) * 2 + (i & 1)];
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
       const float base = m[r] == -INFINITY ? 0.0f : m[r];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float& v = s[t][2 * r + x];
-          v = ex2_approx(v - base);
+        for (int hf = 0; hf < 2; ++hf) {
+          float& v = s[r >> 1][t][2 * hf + (r & 1)];
+          v = ex2_approx(fmaf(v, s2[r], -base));
           l[r] += v;
         }
     }
-    // o += p v.  With up to 8 heads the lower 8 rows of the instruction carry the rest of p's rounding to 16 bits,
-    // so p keeps 16 bits or more; with more heads p is rounded once (bf16: 2^-9 of each weight on average a
-    // quarter of it, below the output's own rounding)
+    // o^T += v^T p^T: 16 columns by 8 heads a tile, 16 keys at a time
 #pragma unroll
-    for (int kk = 0; kk < KT / 16; ++kk) {
-      uint32_t a[4];
+    for (int t = 0; t < MT; ++t) {
+      uint32_t b[NH][2], low[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float(&v)[4] = s[2 * kk + x];
-        a[2 * x] = pack2<F16>(v[0], v[1]);
-        if constexpr (WIDE) {
-          a[2 * x + 1] = pack2<F16>(v[2], v[3]);
-        } else {
-          float2 f;
-          if constexpr (F16)
-            f = __half22float2(*reinterpret_cast<const __half2*>(&a[2 * x]));
-          else
-            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a[2 * x]));
-          a[2 * x + 1] = pack2<F16>(v[0] - f.x, v[1] - f.y);
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float p0 = s[nh][t][2 * hf], p1 = s[nh][t][2 * hf + 1];
+          uint32_t hi = pack2<F16>(p0, p1);
+          if constexpr (LOW_COLS || LOW_MMA) {
+            const float2 f = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&hi))
+                                 : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
+            const uint32_t lo = pack2<F16>(p0 - f.x, p1 - f.y);
+            if constexpr (LOW_COLS)
+              hi = lane & 2 ? lo : hi;
+            else
+              low[hf] = transpose8x8(lo);
+          }
+          b[nh][hf] = transpose8x8(hi);
         }
-      }
-      const int row = kk * 16 + (lane & 15);
+      const int row = t * 16 + (lane & 7) + ((lane >> 4) << 3);
       if constexpr (!S::E4M3) {
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
-          uint32_t b[4];
-          ldmatrix4<true>(b, vb + staged<PITCH>(row, d * 2 + (lane >> 4)));
-          float(&o0)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * d);
-          float(&o1)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * d + 4);
-          mma16816<F16>(o0, a[0], a[1], a[2], a[3], b[0], b[1]);
-          mma16816<F16>(o1, a[0], a[1], a[2], a[3], b[2], b[3]);
+          uint32_t a[4];
+          ldmatrix4<true>(a, vb + staged<PITCH>(row, d * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            float(&acc)[4] = *reinterpret_cast<float(*)[4]>(o + (nh * (DP / 16) + d) * 4);
+            mma16816<F16>(acc, a[0], a[1], a[2], a[3], b[nh][0], b[nh][1]);
+            if constexpr (LOW_MMA) mma16816<F16>(acc, a[0], a[1], a[2], a[3], low[0], low[1]);
+          }
         }
       } else {
-        // a transposed pair of bytes is two columns of one key: the even columns of 16 make one block of the
-        // output, the odd ones another
+        // a transposed pair of bytes is two columns of one key: the even columns of 16 are the upper rows of a
+        // tile, the odd ones the lower
 #pragma unroll
         for (int d = 0; d < DP / 16; d += 2) {
-          uint32_t b[4];
-          ldmatrix4<true>(b, vb + staged<PITCH>(row, d + (lane >> 4)));
+          uint32_t a[4];
+          ldmatrix4<true>(a, vb + staged<PITCH>(row, d + ((lane >> 3) & 1)));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t x0 = e4m3x2_f16x2(b[2 * u]), x1 = e4m3x2_f16x2(b[2 * u] >> 16);
-            const uint32_t y0 = e4m3x2_f16x2(b[2 * u + 1]), y1 = e4m3x2_f16x2(b[2 * u + 1] >> 16);
-            float(&o0)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * (d + u));
-            float(&o1)[4] = *reinterpret_cast<float(*)[4]>(o + 8 * (d + u) + 4);
-            mma16816<F16>(o0, a[0], a[1], a[2], a[3], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-            mma16816<F16>(o1, a[0], a[1], a[2], a[3], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+            const uint32_t x0 = e4m3x2_f16x2(a[u]), x1 = e4m3x2_f16x2_hi(a[u]);
+            const uint32_t y0 = e4m3x2_f16x2(a[u + 2]), y1 = e4m3x2_f16x2_hi(a[u + 2]);
+            const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+            const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+              float(&acc)[4] = *reinterpret_cast<float(*)[4]>(o + (nh * (DP / 16) + d + u) * 4);
+              mma16816<F16>(acc, a0, a1, a2, a3, b[nh][0], b[nh][1]);
+            }
           }
         }
       }
@@ -648,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
   };
 
   // One tile in fp32: 32 / KT lanes share a key's columns, then each lane takes DP / 32 columns of o.
-  auto tile_f32 = [&](int stage) {
+  auto tile_f32 = [&](int stage, uint32_t mask) {
     constexpr int PARTS = 32 / (KT < 32 ? KT : 32), NC = DP / 32;
     const uint8_t* kb = smem + w * ST * S::STAGE + stage * S::STAGE;
     const uint8_t* vb = kb + KT * PITCH;
@@ -665,7 +691,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
         s[g] += (k.x * x.x + k.y * x.y) + (k.z * x.z + k.w * x.w);
       }
     }
-    const bool there = (s_mask[w][stage][0] >> key) & 1u;
+    const bool there = (mask >> key) & 1u;
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
 #pragma unroll
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
     __syncwarp();
   };
 
-  // This lane's elements of o: f(row, column, value index); mma without WIDE: value i and i + 2 are one element.
+  // This lane's elements of o: f(row, column, value index); and the row of state r.
   auto each = [&](auto&& f) {
     if constexpr (S::F32) {
       constexpr int NC = DP / 32;
@@ -725,43 +751,36 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
         for (int i = 0; i < NC; ++i) f(g, NC == 2 ? 2 * lane + i : 4 * lane + 128 * (i / 4) + i % 4, g * NC + i);
     } else {
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int c4 = lane & 3;
-            const int d = S::E4M3 ? (i / 2) * 16 + 4 * c4 + 2 * x + (i & 1) : i * 8 + 2 * c4 + x;
-            f((lane >> 2) + 8 * r, d, 4 * i + 2 * r + x);
-          }
+      for (int i = 0; i < OW; ++i) {
+        const int nh = i / (DP / 4), d = i % (DP / 4) / 4 * 16, hf = (i >> 1) & 1;
+        f(nh * 8 + 2 * (lane & 3) + (i & 1), d + (S::E4M3 ? 2 * (lane >> 2) + hf : 8 * hf + (lane >> 2)), i);
+      }
     }
   };
+  auto row_of = [&](int r) { return S::F32 ? r : (r >> 1) * 8 + 2 * (lane & 3) + (r & 1); };
   // (m, l, o) of this warp into or out of join buffer b
   auto put = [&](int b) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int row = S::F32 ? r : (lane >> 2) + 8 * r;
-      if (S::F32 ? lane == 0 : (lane & 3) == 0) {
-        s_ml[b][row][0] = m[r];
-        s_ml[b][row][1] = l[r];
+    for (int r = 0; r < NR; ++r)
+      if (lane < (S::F32 ? 1 : 4)) {
+        s_ml[b][row_of(r)][0] = m[r];
+        s_ml[b][row_of(r)][1] = l[r];
       }
-    }
-    each([&](int row, int d, int i) { s_o[(b * RG + row) * DP + d] = o[i]; });
+    each([&](int row, int d, int i) { s_o[(b * RG + row) * OS + d] = o[i]; });
   };
   auto take = [&](int b) {
     float c[NR], c2[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int row = S::F32 ? r : (lane >> 2) + 8 * r;
-      const float m2 = s_ml[b][row][0], mn = fmaxf(m[r], m2), base = mn == -INFINITY ? 0.0f : mn;
+      const float m2 = s_ml[b][row_of(r)][0], mn = fmaxf(m[r], m2), base = mn == -INFINITY ? 0.0f : mn;
       c[r] = ex2_approx(m[r] - base);
       c2[r] = ex2_approx(m2 - base);
       m[r] = mn;
-      l[r] = l[r] * c[r] + s_ml[b][row][1] * c2[r];
+      l[r] = l[r] * c[r] + s_ml[b][row_of(r)][1] * c2[r];
     }
     each([&](int row, int d, int i) {
-      const int r = S::F32 ? i / (DP / 32) : (i >> 1) & (NR - 1);
-      o[i] = o[i] * c[r] + s_o[(b * RG + row) * DP + d] * c2[r];
+      const int r = S::F32 ? i / (DP / 32) : i / (DP / 4) * 2 + (i & 1);
+      o[i] = o[i] * c[r] + s_o[(b * RG + row) * OS + d] * c2[r];
     });
   };
 
@@ -792,16 +811,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
   auto end_item = [&](int64_t first_tile, int64_t last_tile) {  // of the whole item, among all T
     if constexpr (!S::F32) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      }
-      if constexpr (!WIDE) {
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          o[4 * i] += o[4 * i + 2];
-          o[4 * i + 1] += o[4 * i + 3];
-        }
+        for (int x = 4; x < 32; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+      if constexpr (LOW_COLS) {
+#pragma unroll
+        for (int i = 0; i < OW; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
       }
     } else {
 #pragma unroll
@@ -821,8 +836,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
       mm = fmaxf(m0, m1);
       const float base = mm == -INFINITY ? 0.0f : mm, c0 = ex2_approx(m0 - base), c1 = ex2_approx(m1 - base);
       ll = s_ml[0][r][1] * c0 + s_ml[1][r][1] * c1;
-      const float4 a = *reinterpret_cast<const float4*>(s_o + r * DP + d);
-      const float4 b = *reinterpret_cast<const float4*>(s_o + (RG + r) * DP + d);
+      const float4 a = *reinterpret_cast<const float4*>(s_o + r * OS + d);
+      const float4 b = *reinterpret_cast<const float4*>(s_o + (RG + r) * OS + d);
       return make_float4(a.x * c0 + b.x * c1, a.y * c0 + b.y * c1, a.z * c0 + b.z * c1, a.w * c0 + b.w * c1);
     };
     // blocks that share the item: the one of its first tile to the one of its last
@@ -863,17 +878,33 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
           const int r = i / vecs, d = (i % vecs) * 4;
           float mm = -INFINITY, ll = 0.0f;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int c = wf; c <= wl; ++c) {
-            const float* part = part_of(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + r * 4));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + gsize * 4 + r * p.head_dim + d));
-            const float mn = fmaxf(mm, ml.x), base = mn == -INFINITY ? 0.0f : mn;
-            const float c0 = ex2_approx(mm - base), c1 = ex2_approx(ml.x - base);
+          constexpr int NB = 8;  // parts read at a time
+          for (int c0 = wf; c0 <= wl; c0 += NB) {
+            float2 ml[NB];
+            float4 v[NB];
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {
+              ml[u] = make_float2(-INFINITY, 0.0f);
+              v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (c0 + u <= wl) {
+                const float* part = part_of(c0 + u);
+                ml[u] = __ldcg(reinterpret_cast<const float2*>(part + r * 4));
+                v[u] = __ldcg(reinterpret_cast<const float4*>(part + gsize * 4 + r * p.head_dim + d));
+              }
+            }
+            float mn = mm;
+#pragma unroll
+            for (int u = 0; u < NB; ++u) mn = fmaxf(mn, ml[u].x);
+            const float base = mn == -INFINITY ? 0.0f : mn, k = ex2_approx(mm - base);
             mm = mn;
-            ll = ll * c0 + ml.y * c1;
-            acc = make_float4(acc.x * c0 + v.x * c1, acc.y * c0 + v.y * c1, acc.z * c0 + v.z * c1,
-                              acc.w * c0 + v.w * c1);
+            ll *= k;
+            acc = make_float4(acc.x * k, acc.y * k, acc.z * k, acc.w * k);
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {
+              const float f = ex2_approx(ml[u].x - base);
+              ll += ml[u].y * f;
+              acc = make_float4(acc.x + v[u].x * f, acc.y + v[u].y * f, acc.z + v[u].z * f, acc.w + v[u].w * f);
+            }
           }
           write_row(r, d, acc, mm, ll);
         }
@@ -894,13 +925,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
       if (i + ST < n) look_up();
     }
     cp_async_commit();
-    bool any = s_mask[w][stage][0] != 0u;
-    if constexpr (KPL == 2) any |= s_mask[w][stage][1] != 0u;
-    if (any) {
+    const uint32_t mask = s_mask[w][stage];
+    if (mask != 0u) {
       if constexpr (S::F32)
-        tile_f32(stage);
+        tile_f32(stage, mask);
       else
-        tile_mma(stage);
+        tile_mma(stage, mask);
     }
     if (at.t + 1 == at.nt || i + 1 == n) {
       end_item(item, item + at.nt - 1);
@@ -916,10 +946,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, WIDE>::CTAS)
   if (bad_page) atomicOr(&g_paged_status, kDevBadIndex);
 }
 
-template <class T, class C, int DP, bool WIDE>
+template <class T, class C, int DP, Heads HEADS>
 cudaError_t run_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
-  using S = AttnShape<T, C, DP, WIDE>;
-  const void* k = reinterpret_cast<const void*>(attention_kernel<T, C, DP, WIDE>);
+  using S = AttnShape<T, C, DP, HEADS>;
+  const void* k = reinterpret_cast<const void*>(attention_kernel<T, C, DP, HEADS>);
   static std::atomic<uint64_t> configured{0};  // a bit for each device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -930,7 +960,7 @@ cudaError_t run_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
     if (dev < 64) configured.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
   const int G = p.q_heads / p.kv_heads;
-  const int64_t units = static_cast<int64_t>(p.kv_heads) * ((G + S::RG - 1) / S::RG);
+  const int64_t units = static_cast<int64_t>(p.kv_heads) * ((G + S::MAXG - 1) / S::MAXG);
   const int64_t tiles = (static_cast<int64_t>(p.max_pages) * p.page_size + S::CT - 1) / S::CT;
   int64_t grid = static_cast<int64_t>(device_sm_count()) * S::CTAS;
   if (grid > kMaxWorkers) grid = kMaxWorkers;
@@ -940,13 +970,23 @@ cudaError_t run_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
   return launch_ex(k, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), S::SMEM, s, pdl, args);
 }
 
+template <class T, class C, Heads HEADS>
+cudaError_t pick_width(const AttnParams& p, cudaStream_t s, bool pdl) {
+  if (p.head_dim <= 64) return run_attention<T, C, 64, HEADS>(p, s, pdl);
+  if (p.head_dim <= 128) return run_attention<T, C, 128, HEADS>(p, s, pdl);
+  return run_attention<T, C, 256, HEADS>(p, s, pdl);
+}
+
 template <class T, class C>
 cudaError_t pick_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
-  const bool wide = p.q_heads / p.kv_heads > (sizeof(T) == 4 ? 1 : 8);
-  if (p.head_dim <= 64) return wide ? run_attention<T, C, 64, true>(p, s, pdl) : run_attention<T, C, 64, false>(p, s, pdl);
-  if (p.head_dim <= 128)
-    return wide ? run_attention<T, C, 128, true>(p, s, pdl) : run_attention<T, C, 128, false>(p, s, pdl);
-  return wide ? run_attention<T, C, 256, true>(p, s, pdl) : run_attention<T, C, 256, false>(p, s, pdl);
+  const int G = p.q_heads / p.kv_heads;
+  if constexpr (sizeof(T) == 4) {
+    return G == 1 ? pick_width<T, C, kFew>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
+  } else {
+    if constexpr (sizeof(C) == 2)  // f16 weights need no second part: kFew is for bf16
+      if (G <= 4) return pick_width<T, C, kFew>(p, s, pdl);
+    return G <= 8 ? pick_width<T, C, kSome>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
+  }
 }
 
 }  // namespace

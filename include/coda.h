@@ -429,7 +429,8 @@ CODA_API coda_status coda_gemm_swiglu_backward(const void* dOut, const void* Wt,
  *   coda_quantize_e4m3.
  *   head_dim: at most 256, a multiple of 4 (fp32), 8 (bf16) or 16 (e4m3
  *   cache).  q_heads: a multiple of kv_heads; query head h reads key/value
- *   head h / (q_heads / kv_heads).  page_size, num_pages >= 1.
+ *   head h / (q_heads / kv_heads).  page_size, num_pages >= 1, and a cache
+ *   has fewer than 2^31 rows (num_pages * kv_heads * page_size).
  *   row_seq [M] int32: the sequence of each row, or NULL when row i belongs
  *   to sequence i (M <= num_seqs then).  Several rows may belong to one
  *   sequence.
