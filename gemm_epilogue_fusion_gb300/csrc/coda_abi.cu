@@ -1212,6 +1212,9 @@ coda_status coda_paged_attention(const void* Q, int64_t ldq, const void* Kc, con
   p.head_dim = static_cast<int>(head_dim);
   p.num_pages = static_cast<int>(num_pages);
   p.page_size = static_cast<int>(page_size);
+  p.page_shift = -1;
+  for (int b = 0; b < 31; ++b)
+    if (page_size == int64_t(1) << b) p.page_shift = b;
   cudaError_t e = coda::launch_paged_attention(p, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
   return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_paged_attention launch");
 }

@@ -188,6 +188,7 @@ struct AttnParams {
   void* workspace;
   float scale;
   int M, num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size;
+  int page_shift;  // log2(page_size), or -1
 };
 cudaError_t launch_paged_append(const AppendParams& p, int64_t M, bool f32, bool e4m3, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl);

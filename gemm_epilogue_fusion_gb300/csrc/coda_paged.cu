@@ -186,6 +186,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxWorkers = 512;  // blocks of a grid: bounds the workspace
 constexpr int kMinTiles = 2;      // tiles a block takes at least
+constexpr int kFlatJoin = 24;     // parts of an item joined at once (see the kernel's end)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 
@@ -285,6 +286,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ unsigned atom_add_acq_rel_gpu(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // What the kernel knows of a row: keys that count, and its sequence.
 struct RowInfo {
   int len, seq;
@@ -325,6 +332,71 @@ struct Cursor {
   }
 };
 
+// a / b; the 64-bit division is a long subroutine, so numbers that fit take the 32-bit one.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// T tiles dealt to the blocks that take part: runs of `per` tiles, the first `more` runs one longer.
+struct Runs {
+  int64_t T, per;
+  int workers, more;
+  __device__ __forceinline__ void set(int64_t tiles, int grid) {
+    T = tiles;
+    workers = static_cast<int>(min(static_cast<int64_t>(grid), max(T / kMinTiles, static_cast<int64_t>(1))));
+    per = div_small(T, workers);
+    more = static_cast<int>(T - per * workers);
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return per * c + min(c, more); }
+  __device__ __forceinline__ int owner(int64_t i) const {  // the block of tile i
+    const int64_t longer = (per + 1) * more;
+    return static_cast<int>(i < longer ? div_small(i, per + 1) : more + div_small(i - longer, per));
+  }
+};
+
+// The parts of a shared item joined in the order of the keys: the first, and
+// `more` others that lie `stride` floats apart, the last of them at `last`.
+// (m, l) is at `ml`, four columns of o at `v` of each.  8 parts are read at a
+// time (16 take registers from the loop over the keys): what this costs is a
+// trip to L2, about 1 us, for each batch.
+struct Part {
+  float m, l;
+  float4 v;
+};
+__device__ __forceinline__ Part join_parts(const float* first, const float* last, int more, int64_t stride, int ml, int v) {
+  constexpr int NB = 8;
+  Part a = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (int c0 = 0; c0 <= more; c0 += NB) {
+    float2 s[NB];
+    float4 x[NB];
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      s[u] = make_float2(-INFINITY, 0.0f);
+      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c0 + u <= more) {
+        const float* part = c0 + u == 0 ? first : last - (more - c0 - u) * stride;
+        s[u] = __ldcg(reinterpret_cast<const float2*>(part + ml));
+        x[u] = __ldcg(reinterpret_cast<const float4*>(part + v));
+      }
+    }
+    float mn = a.m;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) mn = fmaxf(mn, s[u].x);
+    const float base = mn == -INFINITY ? 0.0f : mn, k = ex2_approx(a.m - base);
+    a.m = mn;
+    a.l *= k;
+    a.v = make_float4(a.v.x * k, a.v.y * k, a.v.z * k, a.v.w * k);
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const float f = ex2_approx(s[u].x - base);
+      a.l += s[u].y * f;
+      a.v = make_float4(a.v.x + x[u].x * f, a.v.y + x[u].y * f, a.v.z + x[u].z * f, a.v.w + x[u].w * f);
+    }
+  }
+  return a;
+}
+
 template <class E, class C, int DP, Heads HEADS>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
@@ -350,8 +422,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   pdl_launch_dependents();
 
   // ---- this block's run of tiles: [i0, i1) of T, in the order (row, unit, tile)
-  int64_t T, i0, i1;
-  int workers;
+  Runs run;
+  int64_t i0, i1;
   {
     const int per = (p.M + kAttnThreads - 1) / kAttnThreads;
     const int r0 = min(tid * per, p.M), r1 = min(r0 + per, p.M);
@@ -373,19 +445,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       if (x < w) before += s_scan[x];
       total += s_scan[x];
     }
-    T = total * units;
-    workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(T / kMinTiles, static_cast<int64_t>(1))));
-    if (static_cast<int>(blockIdx.x) >= workers) return;
-    i0 = T * blockIdx.x / workers;
-    i1 = T * (blockIdx.x + 1) / workers;
+    run.set(total * units, gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= run.workers) return;
+    i0 = run.first(blockIdx.x);
+    i1 = run.first(blockIdx.x + 1);
     int64_t at = (before + incl - sum) * units;  // first tile of this thread's rows
     if (i0 >= at && i0 < at + sum * units) {
       for (int r = r0; r < r1; ++r) {
         const int nt = max(1, (row_info(p, r, bad).len + CT - 1) / CT);
         if (i0 < at + static_cast<int64_t>(nt) * units) {
           s_start[0] = r;
-          s_start[1] = static_cast<int>((i0 - at) / nt);
-          s_start[2] = static_cast<int>((i0 - at) % nt);
+          s_start[1] = static_cast<int>(div_small(i0 - at, nt));
+          s_start[2] = static_cast<int>(i0 - at) - s_start[1] * nt;
           break;
         }
         at += static_cast<int64_t>(nt) * units;
@@ -409,7 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     pg = -1;
     slot = -1;  // no such key
     if (lane < KT && key < in.len) {
-      const int q = key / p.page_size;
+      const int q = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
       slot = key - q * p.page_size;
       pg = __ldg(p.page_table + static_cast<int64_t>(in.seq) * p.max_pages + q);
     }
@@ -784,10 +855,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     });
   };
 
-  // Counters [kMaxWorkers], then per block two parts of (m, l) [gsize] and o [gsize][head_dim]
+  // Counters [2][kMaxWorkers], then per block two parts of (m, l) [gsize] and o [gsize][head_dim]
   unsigned* counters = static_cast<unsigned*>(p.workspace);
   const int part_floats = gsize * (p.head_dim + 4);
-  float* parts = reinterpret_cast<float*>(counters + kMaxWorkers);
+  float* parts = reinterpret_cast<float*>(counters + 2 * kMaxWorkers);
 
   auto write_row = [&](int r, int d, float4 v, float mm, float ll) {
     const int hk = at.h / groups, g0 = (at.h % groups) * gsize;
@@ -840,8 +911,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       const float4 b = *reinterpret_cast<const float4*>(s_o + (RG + r) * OS + d);
       return make_float4(a.x * c0 + b.x * c1, a.y * c0 + b.y * c1, a.z * c0 + b.z * c1, a.w * c0 + b.w * c1);
     };
-    // blocks that share the item: the one of its first tile to the one of its last
-    auto worker_of = [&](int64_t i) { return static_cast<int>(((i + 1) * workers - 1) / T); };
     const bool whole = first_tile >= i0 && last_tile < i1;
     if (whole) {
       for (int i = tid; i < ng * vecs; i += kAttnThreads) {
@@ -851,11 +920,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         write_row(r, d, v, mm, ll);
       }
     } else {
-      const int wf = worker_of(first_tile), wl = worker_of(last_tile);
-      auto part_of = [&](int c) {  // an item begun in block c behind its first tile is that block's second part
-        const int second = c == wf && first_tile > T * c / workers;
-        return parts + (static_cast<int64_t>(c) * 2 + second) * part_floats;
-      };
+      // blocks that share the item; one begun in block wf behind its first tile is that block's second part
+      const int wf = run.owner(first_tile), wl = run.owner(last_tile);
+      const int second = first_tile > run.first(wf);
+      auto part_of = [&](int c) { return parts + (2 * c + (c == wf ? second : 0)) * static_cast<int64_t>(part_floats); };
       float* mine = part_of(blockIdx.x);
       for (int i = tid; i < ng * vecs; i += kAttnThreads) {
         const int r = i / vecs, d = (i % vecs) * 4;
@@ -864,51 +932,50 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         __stcg(reinterpret_cast<float4*>(mine + gsize * 4 + r * p.head_dim + d), v);
         if (d == 0) __stcg(reinterpret_cast<float2*>(mine + r * 4), make_float2(mm, ll));
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned arrived = atomicAdd(counters + wf, 1u);
-        s_last = arrived == static_cast<unsigned>(wl - wf);
-        if (s_last) counters[wf] = 0;  // ready for the next call
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
+      // The block that comes last of `others` + 1: its parts released (ordered before by the barrier), theirs acquired.
+      auto comes_last = [&](unsigned* counter, int others) {
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atom_add_acq_rel_gpu(counter, 1u) == static_cast<unsigned>(others);
+          if (s_last) *counter = 0;  // ready for the next call
+        }
+        __syncthreads();
+        return s_last != 0;
+      };
+      // Parts c, c + step, ... (`more` of them behind c) joined: f(row, column, result)
+      auto join = [&](int c, int step, int more, auto&& f) {
         for (int i = tid; i < ng * vecs; i += kAttnThreads) {
           const int r = i / vecs, d = (i % vecs) * 4;
-          float mm = -INFINITY, ll = 0.0f;
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          constexpr int NB = 8;  // parts read at a time
-          for (int c0 = wf; c0 <= wl; c0 += NB) {
-            float2 ml[NB];
-            float4 v[NB];
-#pragma unroll
-            for (int u = 0; u < NB; ++u) {
-              ml[u] = make_float2(-INFINITY, 0.0f);
-              v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (c0 + u <= wl) {
-                const float* part = part_of(c0 + u);
-                ml[u] = __ldcg(reinterpret_cast<const float2*>(part + r * 4));
-                v[u] = __ldcg(reinterpret_cast<const float4*>(part + gsize * 4 + r * p.head_dim + d));
+          f(r, d, join_parts(part_of(c), part_of(c + more * step), more, 2 * step * static_cast<int64_t>(part_floats),
+                             r * 4, gsize * 4 + r * p.head_dim + d));
+        }
+      };
+      const int count = wl - wf + 1;
+      int step = 1;
+      bool mine_last = true;
+      if (count > kFlatJoin) {
+        // many parts: groups of neighbours first, each joined into its first part, most of them long before the end
+        step = count <= 8 * kFlatJoin / 3 ? 8 : 16;
+        const int c = wf + (static_cast<int>(blockIdx.x) - wf) / step * step, more = min(step - 1, wl - c);
+        if (more > 0) {
+          mine_last = comes_last(counters + kMaxWorkers + c, more);
+          if (mine_last) {
+            float* to = part_of(c);
+            join(c, 1, more, [&](int r, int d, const Part& j) {
+              __stcg(reinterpret_cast<float4*>(to + gsize * 4 + r * p.head_dim + d), j.v);
+              if (d == 0) {
+                s_ml[0][r][0] = j.m;
+                s_ml[0][r][1] = j.l;
               }
-            }
-            float mn = mm;
-#pragma unroll
-            for (int u = 0; u < NB; ++u) mn = fmaxf(mn, ml[u].x);
-            const float base = mn == -INFINITY ? 0.0f : mn, k = ex2_approx(mm - base);
-            mm = mn;
-            ll *= k;
-            acc = make_float4(acc.x * k, acc.y * k, acc.z * k, acc.w * k);
-#pragma unroll
-            for (int u = 0; u < NB; ++u) {
-              const float f = ex2_approx(ml[u].x - base);
-              ll += ml[u].y * f;
-              acc = make_float4(acc.x + v[u].x * f, acc.y + v[u].y * f, acc.z + v[u].z * f, acc.w + v[u].w * f);
-            }
+            });
+            __syncthreads();  // every thread has read the first part's (m, l)
+            if (tid < ng) __stcg(reinterpret_cast<float2*>(to + tid * 4), make_float2(s_ml[0][tid][0], s_ml[0][tid][1]));
           }
-          write_row(r, d, acc, mm, ll);
         }
       }
+      const int groups_of = (count + step - 1) / step;
+      if (mine_last && comes_last(counters + wf, groups_of - 1))
+        join(wf, step, groups_of - 1, [&](int r, int d, const Part& j) { write_row(r, d, j.v, j.m, j.l); });
     }
     __syncthreads();  // the join buffers are free again
   };
@@ -1008,7 +1075,7 @@ cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cud
 // Counters and two parts of at most min(G, 16) heads for each block.
 int64_t paged_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
   const int G = q_heads / kv_heads, rows = G < 16 ? G : 16;
-  return kMaxWorkers * (4 + 2 * static_cast<int64_t>(rows) * (head_dim + 4) * 4);
+  return kMaxWorkers * (8 + 2 * static_cast<int64_t>(rows) * (head_dim + 4) * 4);
 }
 
 unsigned read_clear_status_paged() {
