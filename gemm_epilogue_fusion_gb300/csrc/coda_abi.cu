@@ -1050,6 +1050,13 @@ coda_status coda_get_device_status(void) {
 // ------------------------------------------------- paged cache, attention ----
 namespace {
 
+// log2(n) of a power of two below 2^31, else -1.
+int log2_or_none(int64_t n) {
+  for (int b = 0; b < 31; ++b)
+    if (n == int64_t(1) << b) return b;
+  return -1;
+}
+
 // Shape rules common to the paged cache calls.
 coda_status check_paged(int64_t M, int64_t num_seqs, int64_t max_pages, int64_t q_heads, int64_t kv_heads,
                         int64_t head_dim, int64_t num_pages, int64_t page_size, const int32_t* row_seq,
@@ -1132,6 +1139,8 @@ coda_status coda_paged_append(const void* Z, const int32_t* positions, const int
   p.head_dim = static_cast<int>(head_dim);
   p.num_pages = static_cast<int>(num_pages);
   p.page_size = static_cast<int>(page_size);
+  p.M = M;
+  p.page_shift = log2_or_none(page_size);
   p.rotate = base != 0.0;
   if (p.rotate) {
     // base^(-2j / head_dim) / 2 pi < 1 as a 64-bit fraction of a turn, by repeated products in 64 bits: the
@@ -1141,7 +1150,7 @@ coda_status coda_paged_append(const void* Z, const int32_t* positions, const int
     for (int64_t j = 0; j < head_dim / 2; ++j, f *= ratio) p.turn[j] = static_cast<uint64_t>(f);
   }
   cudaError_t e =
-      coda::launch_paged_append(p, M, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
+      coda::launch_paged_append(p, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
   return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_paged_append launch");
 }
 
@@ -1212,9 +1221,7 @@ coda_status coda_paged_attention(const void* Q, int64_t ldq, const void* Kc, con
   p.head_dim = static_cast<int>(head_dim);
   p.num_pages = static_cast<int>(num_pages);
   p.page_size = static_cast<int>(page_size);
-  p.page_shift = -1;
-  for (int b = 0; b < 31; ++b)
-    if (page_size == int64_t(1) << b) p.page_shift = b;
+  p.page_shift = log2_or_none(page_size);
   cudaError_t e = coda::launch_paged_attention(p, dtype == CODA_F32, cache_dtype == CODA_E4M3, stream, use_pdl());
   return e == cudaSuccess ? CODA_OK : cuda_fail(e, "coda_paged_attention launch");
 }

@@ -168,7 +168,9 @@ struct AppendParams {
   void* Vc;
   const float* scale_k;  // e4m3 caches: dequantisation scales, else null
   const float* scale_v;
+  int64_t M;
   int num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size;
+  int page_shift;  // log2(page_size), or -1
   int rotate;
   // Pair j turns by turn[j] / 2^64 of a whole turn per position: base^(-2j/head_dim) / 2 pi
   uint64_t turn[kMaxHeadDim / 2];
@@ -190,7 +192,7 @@ struct AttnParams {
   int M, num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size;
   int page_shift;  // log2(page_size), or -1
 };
-cudaError_t launch_paged_append(const AppendParams& p, int64_t M, bool f32, bool e4m3, cudaStream_t s, bool pdl);
+cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl);
 int64_t paged_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim);
 unsigned read_clear_status_paged();

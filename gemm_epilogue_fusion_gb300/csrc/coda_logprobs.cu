@@ -44,17 +44,47 @@ __device__ __forceinline__ void pairs(const uint4& w, float2 (&f)[8 / sizeof(E)]
   }
 }
 
-// The largest of 16 bytes of logits.
-template <class E>
-__device__ __forceinline__ float largest(const uint4& w) {
+// The largest of N times 16 bytes of logits.
+template <class E, int N>
+__device__ __forceinline__ float largest(const uint4 (&w)[N]) {
   if constexpr (sizeof(E) == 4) {
-    return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
-                   max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      m = max_nan(m, max_nan(max_nan(__uint_as_float(w[u].x), __uint_as_float(w[u].y)),
+                             max_nan(__uint_as_float(w[u].z), __uint_as_float(w[u].w))));
+    return m;
+  } else {
+    __nv_bfloat162 m[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w[u]);
+      m[u] = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+      if (u > 0) m[0] = __hmax2_nan(m[0], m[u]);
+    }
+    return max_nan(__low2float(m[0]), __high2float(m[0]));
+  }
+}
+
+// Logits of this size or more take the careful path: times log2 e they could
+// leave fp32's range.  A power of two that bf16 holds.
+constexpr float kHuge = 0x1p126f;
+
+// 16 bytes of logits, none below -kHuge (NaN stays).
+template <class E>
+__device__ __forceinline__ uint4 lifted(const uint4& w) {
+  uint4 o;
+  if constexpr (sizeof(E) == 4) {
+    o = make_uint4(__float_as_uint(max_nan(__uint_as_float(w.x), -kHuge)), __float_as_uint(max_nan(__uint_as_float(w.y), -kHuge)),
+                   __float_as_uint(max_nan(__uint_as_float(w.z), -kHuge)), __float_as_uint(max_nan(__uint_as_float(w.w), -kHuge)));
   } else {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
-    return max_nan(__low2float(m), __high2float(m));
+    __nv_bfloat162* r = reinterpret_cast<__nv_bfloat162*>(&o);
+    const __nv_bfloat162 low = __floats2bfloat162_rn(-kHuge, -kHuge);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = __hmax2_nan(h[e], low);
   }
+  return o;
 }
 
 // Vector v of a row of V logits; elements behind the row are -inf.
@@ -109,6 +139,7 @@ struct Sums {
   }
 };
 
+constexpr int kRowThreads = 512, kRowVecs = 4;  // threads of a block, vectors of a thread in flight
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 
@@ -142,7 +173,7 @@ struct LogprobsShared {
 // arithmetic is packed in pairs) of the 11 that the HBM rate leaves.
 template <class E, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-  constexpr int VEC = 16 / sizeof(E), U = 4;
+  constexpr int VEC = 16 / sizeof(E), U = kRowVecs;
   __shared__ LogprobsShared<NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0, ranks = CLUSTER ? p.ranks : 1;
@@ -153,62 +184,68 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   const int vecs = (p.V + VEC - 1) / VEC, per = (vecs + ranks - 1) / ranks;
   const int v0 = min(rank * per, vecs), v1 = min(v0 + per, vecs);
 
-  Sums a = {-INFINITY, 0.0f, 0.0f};
-  auto take = [&](const uint4& q) {
-    float2 f[8 / sizeof(E)];
-    pairs<E>(q, f);
-    const float base = a.m == -INFINITY ? 0.0f : a.m;
-    float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      float2 d = fmul2(fadd2(f[e], make_float2(-base, -base)), make_float2(kLog2e, kLog2e));
-      // 2^-200 is 0 in fp32: the clamp only keeps 0 * -inf out of t
-      d.x = max_nan(d.x, -200.0f);
-      d.y = max_nan(d.y, -200.0f);
-      const float2 g = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-      s2 = fadd2(s2, g);
-      t2 = ffma2(g, d, t2);
-    }
-    a.s += s2.x + s2.y;
-    a.t += t2.x + t2.y;
-  };
-  int v = v0 + tid;
-  for (; v + (U - 1) * NT < v1 && (v + (U - 1) * NT + 1) * VEC <= p.V; v += U * NT) {
+  // This thread's running maximum m and sums relative to base = m log2 e, two of each side by side: d = x log2 e - base
+  // is one operation for two elements.  -inf and huge negative logits are lifted to -2^126, whose weight is 0 as well.
+  float m = -INFINITY, base = 0.0f;
+  float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
+  const int whole = min(v1, p.V / VEC);  // vectors without an end of the row inside
+  for (int v = v0 + tid; v < v1; v += U * NT) {
     uint4 q[U];
+    if (v + (U - 1) * NT < whole) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
-    float big = largest<E>(q[0]);
+      for (int u = 0; u < U; ++u) q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
+    } else {
+      // the last round: what lies behind the row or this block's part of it is -inf
 #pragma unroll
-    for (int u = 1; u < U; ++u) big = max_nan(big, largest<E>(q[u]));
-    if (!(big <= a.m)) a.raise(max_nan(a.m, big));
+      for (int u = 0; u < U; ++u) {
+        if (v + u * NT < whole)
+          q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
+        else
+          q[u] = load_vec<E>(x, v + u * NT < v1 ? v + u * NT : vecs, p.V);
+      }
+    }
+    const float big = largest<E, U>(q);
+    if (!(big <= m)) {
+      m = max_nan(m, big);
+      const float to = fminf(fmaxf(m, -kHuge), kHuge) * kLog2e, d = base - to, c = ex2_approx(d);
+      // the first time there is nothing to scale (and c may be infinite); a weight of 0 ends what was summed
+      const bool none = c == 0.0f || s2.x + s2.y == 0.0f;
+      t2 = none ? make_float2(0.0f, 0.0f) : fmul2(ffma2(s2, make_float2(d, d), t2), make_float2(c, c));
+      s2 = none ? make_float2(0.0f, 0.0f) : fmul2(s2, make_float2(c, c));
+      base = to;
+    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) take(q[u]);
+    for (int u = 0; u < U; ++u) {
+      float2 f[8 / sizeof(E)];
+      pairs<E>(lifted<E>(q[u]), f);
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 d = ffma2(f[e], make_float2(kLog2e, kLog2e), make_float2(-base, -base));
+        const float2 g = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+        s2 = fadd2(s2, g);
+        t2 = ffma2(g, d, t2);
+      }
+    }
   }
-  for (; v < v1; v += NT) {
-    const uint4 q = load_vec<E>(x, v, p.V);
-    const float big = largest<E>(q);
-    if (!(big <= a.m)) a.raise(max_nan(a.m, big));
-    take(q);
+  // the sums relative to m itself: base was rounded by `off`
+  Sums a = {m, s2.x + s2.y, t2.x + t2.y};
+  if (!(m < INFINITY)) {
+    a.s = a.t = NAN;  // +inf or NaN
+  } else if (fabsf(m) > kHuge) {
+    a.s = a.t = 0.0f;  // no weight beside an ordinary logit (and see `careful`)
+  } else {
+    const float off = fmaf(m, kLog2e, -base), c = ex2_approx(-off);
+    a.t = (a.t - off * a.s) * c;
+    a.s *= c;
   }
-  if (p.top > 0) sh.key[tid] = v0 + tid < v1 ? value_key(a.m) : 0u;
+  if (p.top > 0) sh.key[tid] = v0 + tid < v1 ? value_key(m) : 0u;
   if (tid == 0) {
     sh.owners = 0;
     sh.found = 0;
   }
 
   // ---- the row's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
-    a.add(b);
-  }
-  if (lane == 0) sh.warp[w] = a;
-  __syncthreads();
-  if (w == 0) {
-    a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+  auto warp_sums = [&]() {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       Sums b;
@@ -217,29 +254,57 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
       b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
       a.add(b);
     }
-    if (lane == 0) sh.part = a;
-    if (p.top > 0) {
-      // the top-th largest of the threads' keys, bit by bit: bf16 keys differ in their upper 16 bits only
-      uint32_t k[NT / 32], bound = 0;
-#pragma unroll
-      for (int e = 0; e < NT / 32; ++e) k[e] = sh.key[lane + 32 * e];
-      for (int bit = 31; bit >= (sizeof(E) == 4 ? 0 : 16); --bit) {
-        const uint32_t t = bound | (1u << bit);
-        int c = 0;
-#pragma unroll
-        for (int e = 0; e < NT / 32; ++e) c += k[e] >= t;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (c >= p.top) bound = t;
-        if (c == p.top) break;
-      }
-      if (lane == 0) sh.bound = bound;
+  };
+  auto block_sums = [&]() {  // into sh.part, by warp 0
+    warp_sums();
+    if (lane == 0) sh.warp[w] = a;
+    __syncthreads();
+    if (w == 0) {
+      a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+      warp_sums();
+      if (lane == 0) sh.part = a;
     }
+  };
+  block_sums();
+  if (w == 1 && p.top > 0) {
+    // the top-th largest of the threads' keys, bit by bit: bf16 keys differ in their upper 16 bits only
+    uint32_t k[NT / 32], bound = 0;
+#pragma unroll
+    for (int e = 0; e < NT / 32; ++e) k[e] = sh.key[lane + 32 * e];
+    for (int bit = 31; bit >= (sizeof(E) == 4 ? 0 : 16); --bit) {
+      const uint32_t t = bound | (1u << bit);
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < NT / 32; ++e) c += k[e] >= t;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c >= p.top) bound = t;
+      if (c == p.top) break;
+    }
+    if (lane == 0) sh.bound = bound;
+  }
+  __syncthreads();
+  if (fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY) {
+    // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
+    const float top = sh.part.m;
+    a = {top, 0.0f, 0.0f};
+    for (int v = v0 + tid; v < v1; v += NT) {
+      float2 f[8 / sizeof(E)];
+      pairs<E>(load_vec<E>(x, v, p.V), f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = fmaxf(((e & 1 ? f[e / 2].y : f[e / 2].x) - top) * kLog2e, -200.0f), g = ex2_approx(d);
+        a.s += g;
+        a.t += g * d;
+      }
+    }
+    __syncthreads();  // every thread has read sh.part
+    block_sums();
+    __syncthreads();
   }
   int local = 0;  // alternatives this block has: min(top, its elements)
   if (p.top > 0) {
     const int64_t first = static_cast<int64_t>(v0) * VEC, last = min(static_cast<int64_t>(v1) * VEC, static_cast<int64_t>(p.V));
     local = static_cast<int>(min(static_cast<int64_t>(p.top), max(last - first, static_cast<int64_t>(0))));
-    __syncthreads();
     const uint32_t bound = sh.bound;
     if (v0 + tid < v1 && sh.key[tid] >= bound) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
     __syncthreads();
@@ -445,18 +510,18 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const _
   }
 }
 
+// One block per row: NT threads; few rows: clusters of blocks of 512 threads.
 template <class E, int NT>
 cudaError_t run_logprobs(LogprobsParams p, int64_t M, cudaStream_t s, bool pdl) {
-  // few rows: up to 8 blocks (a cluster) share a row, as long as the rows leave SMs idle and each block has at least
-  // one round of loads
-  constexpr int VEC = 16 / sizeof(E);
+  // up to 8 blocks share a row, as long as the rows leave SMs idle and each block has at least one round of loads
+  constexpr int VEC = 16 / sizeof(E), WIDE = 512;
   int c = 1;
-  while (c < kMaxCluster && M * c * 2 <= device_sm_count() && p.V / (c * 2) >= NT * VEC) c *= 2;
+  while (c < kMaxCluster && M * c * 2 <= device_sm_count() && p.V / (c * 2) >= WIDE * VEC) c *= 2;
   p.ranks = c;
   void* args[] = {&p};
-  const void* k = c > 1 ? reinterpret_cast<const void*>(logprobs_kernel<E, NT, true>)
+  const void* k = c > 1 ? reinterpret_cast<const void*>(logprobs_kernel<E, WIDE, true>)
                         : reinterpret_cast<const void*>(logprobs_kernel<E, NT, false>);
-  return launch_ex(k, dim3(static_cast<unsigned>(M * c)), dim3(NT), 0, s, pdl, args, c);
+  return launch_ex(k, dim3(static_cast<unsigned>(M * c)), dim3(c > 1 ? WIDE : NT), 0, s, pdl, args, c);
 }
 
 }  // namespace
@@ -464,7 +529,7 @@ cudaError_t run_logprobs(LogprobsParams p, int64_t M, cudaStream_t s, bool pdl) 
 cudaError_t launch_logprobs(const LogprobsParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl) {
   // short rows take small blocks
   if (p.V <= 8192) return f32 ? run_logprobs<float, 128>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, 128>(p, M, s, pdl);
-  return f32 ? run_logprobs<float, 512>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, 512>(p, M, s, pdl);
+  return f32 ? run_logprobs<float, kRowThreads>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, kRowThreads>(p, M, s, pdl);
 }
 
 int64_t logprobs_backward_blocks(int64_t V, bool f32) {

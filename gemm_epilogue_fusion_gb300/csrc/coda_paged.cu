@@ -56,30 +56,51 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 }
 
 // ------------------------------------------------------------------- append ----
-// One block per row, one thread per 16-byte chunk of a head: a thread keeps its
-// chunk's columns for all the heads it takes, so the sines and cosines of its
-// pairs are computed once a row.  The angle of pair j at position pos is the
-// fraction of a turn turn[j] * pos / 2^64, an exact product that wraps by whole
-// turns by itself; its upper 32 bits go to fp32 (2^-25 of half a turn).  bf16
-// takes the sine and cosine of the special-function unit (2^-21 of 1 on this
-// range, a 32nd of the output's rounding), fp32 the accurate ones.
-// Bound by the bytes of Z, Q and the new slots; the loads of a row's heads are
-// issued before its position and page are known.
-constexpr int kAppendThreads = 128, kAppendHeads = 6;  // heads of a thread in flight
+// A block takes rows in turn, one thread per 16-byte chunk of a head: a thread
+// keeps its chunk's columns for all the heads it takes, so the sines and
+// cosines of its pairs are computed once a row.  The angle of pair j at
+// position pos is the fraction of a turn turn[j] * pos / 2^64, an exact product
+// that wraps by whole turns by itself; its upper 32 bits go to fp32 (2^-25 of
+// half a turn).  bf16 takes the sine and cosine of the special-function unit
+// (2^-21 of 1 on this range, a 32nd of the output's rounding), fp32 the
+// accurate ones.
+// Bound by the bytes of Z, Q and the new slots: a row's heads are loaded while
+// its angles are computed, and its position and page are read a row ahead.
+constexpr int kAppendThreads = 128, kAppendHeads = 3;  // heads of a thread in flight
+constexpr int kAppendBlocks = 8;  // blocks of a launch for each SM: as many as fit one
+
+// What a row needs to know: its position (< 0: left out) and page.
+struct AppendRow {
+  int pos, page;
+};
+__device__ __forceinline__ AppendRow append_row(const AppendParams& p, int64_t i, int64_t M) {
+  AppendRow r = {-1, -1};
+  if (i >= M) return r;
+  r.pos = __ldg(p.positions + i);
+  const int seq = p.row_seq ? __ldg(p.row_seq + i) : static_cast<int>(i);
+  if (r.pos < 0) return r;
+  const int at = p.page_shift >= 0 ? r.pos >> p.page_shift : r.pos / p.page_size;
+  if (seq >= 0 && seq < p.num_seqs && at < p.max_pages)
+    r.page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.max_pages + at);
+  return r;
+}
 
 template <class E, class C>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int VEC = 16 / sizeof(E);
   const int chunks = p.head_dim / VEC, heads = p.q_heads + 2 * p.kv_heads, lanes = kAppendThreads / chunks;
   const int c = threadIdx.x % chunks, h0 = threadIdx.x / chunks;
-  const int64_t i = blockIdx.x;
+  uint64_t turn[VEC / 2];
+  if (p.rotate) {
+    // by its generic address: the threads' chunks differ, and the constant cache serves one address at a time
+    const uint64_t* t = p.turn + c * (VEC / 2);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) asm volatile("ld.u64 %0, [%1];" : "=l"(turn[e]) : "l"(t + e));
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (h0 >= lanes) return;
-  const int pos = p.positions[i];
-  const int seq = p.row_seq ? p.row_seq[i] : static_cast<int>(i);
-  const uint4* z = reinterpret_cast<const uint4*>(static_cast<const E*>(p.Z) + i * heads * p.head_dim) + c;
-  float s[VEC / 2], co[VEC / 2], inv_k = 0.0f, inv_v = 0.0f, sk = 1.0f, sv = 1.0f;
+  float inv_k = 0.0f, inv_v = 0.0f, sk = 1.0f, sv = 1.0f;
   bool fast = true;
   if constexpr (sizeof(C) == 1) {
     sk = *p.scale_k;
@@ -88,73 +109,78 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     inv_k = __frcp_rn(sk);
     inv_v = __frcp_rn(sv);
   }
-  int64_t slot = -1;  // row of the caches for head 0; -2: an index out of range
-  for (int hb = h0; hb < heads; hb += lanes * kAppendHeads) {
-    uint4 w[kAppendHeads];
-#pragma unroll
-    for (int u = 0; u < kAppendHeads; ++u) {
-      const int h = hb + u * lanes;
-      if (h < heads) w[u] = __ldg(z + static_cast<int64_t>(h) * chunks);
+  AppendRow next = append_row(p, blockIdx.x, p.M);
+  for (int64_t i = blockIdx.x; i < p.M; i += gridDim.x) {
+    const AppendRow row = next;
+    next = append_row(p, i + gridDim.x, p.M);
+    if (row.pos < 0) continue;
+    if (row.page < 0 || row.page >= p.num_pages) {
+      if (threadIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
+      continue;
     }
-    if (hb == h0) {
-      if (pos < 0) return;
-      int page = -1;
-      if (seq >= 0 && seq < p.num_seqs && pos / p.page_size < p.max_pages)
-        page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.max_pages + pos / p.page_size);
-      if (p.rotate) {
+    const int in_page = p.page_shift >= 0 ? row.pos & (p.page_size - 1) : row.pos % p.page_size;
+    const uint4* z = reinterpret_cast<const uint4*>(static_cast<const E*>(p.Z) + i * heads * p.head_dim) + c;
+    E* const q = static_cast<E*>(p.Q) + (p.Q ? i * p.q_heads * p.head_dim + c * VEC : 0);
+    // elements of the caches before this row's slot of head 0
+    const int64_t slot = (static_cast<int64_t>(row.page) * p.kv_heads * p.page_size + in_page) * p.head_dim + c * VEC;
+    float s[VEC / 2], co[VEC / 2];
+    for (int hb = h0; hb < heads; hb += lanes * kAppendHeads) {
+      uint4 w[kAppendHeads];
+#pragma unroll
+      for (int u = 0; u < kAppendHeads; ++u)
+        if (hb + u * lanes < heads) w[u] = __ldcs(z + (hb + u * lanes) * chunks);
+      if (p.rotate && hb == h0) {
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) {
-          const int turn = static_cast<int>((p.turn[c * (VEC / 2) + e] * static_cast<uint64_t>(pos)) >> 32);
-          const float half_turns = static_cast<float>(turn) * 0x1p-31f;
+          const int t = static_cast<int>((turn[e] * static_cast<uint64_t>(row.pos)) >> 32);
+          const float half_turns = static_cast<float>(t) * 0x1p-31f;
           if constexpr (sizeof(E) == 4)
             sincospif(half_turns, &s[e], &co[e]);
           else
             __sincosf(half_turns * 3.14159265358979f, &s[e], &co[e]);
         }
       }
-      if (page < 0 || page >= p.num_pages) {
-        if (threadIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
-        return;
-      }
-      slot = static_cast<int64_t>(page) * p.kv_heads * p.page_size + pos % p.page_size;
-    }
 #pragma unroll
-    for (int u = 0; u < kAppendHeads; ++u) {
-      const int h = hb + u * lanes;
-      if (h >= heads) break;
-      if (h < p.q_heads && p.Q == nullptr) continue;
-      const bool is_v = h >= p.q_heads + p.kv_heads;
-      float f[VEC];
-      unpack<E>(w[u], f);
-      if (p.rotate && !is_v) {
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          const float a = f[2 * e], b = f[2 * e + 1];
-          f[2 * e] = a * co[e] - b * s[e];
-          f[2 * e + 1] = a * s[e] + b * co[e];
+      for (int u = 0; u < kAppendHeads; ++u) {
+        const int h = hb + u * lanes;
+        if (h >= heads) break;
+        if (h < p.q_heads && p.Q == nullptr) continue;
+        const int hv = h - p.q_heads - p.kv_heads;  // >= 0: a value head
+        if (hv >= 0 && sizeof(C) == sizeof(E)) {    // values are only laid out
+          *reinterpret_cast<uint4*>(static_cast<C*>(p.Vc) + slot + hv * p.page_size * static_cast<int64_t>(p.head_dim)) = w[u];
+          continue;
         }
-      }
-      if (h < p.q_heads) {
-        reinterpret_cast<uint4*>(static_cast<E*>(p.Q) + (i * p.q_heads + h) * p.head_dim)[c] = pack<E>(f);
-        continue;
-      }
-      const int hk = h - p.q_heads - (is_v ? p.kv_heads : 0);
-      C* dst = static_cast<C*>(is_v ? p.Vc : p.Kc) + (slot + static_cast<int64_t>(hk) * p.page_size) * p.head_dim +
-               c * VEC;
-      if constexpr (sizeof(C) == 1) {
-        const float sc = is_v ? sv : sk, inv = is_v ? inv_v : inv_k;
-        uint32_t o[2];
+        float f[VEC];
+        unpack<E>(w[u], f);
+        if (p.rotate && hv < 0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t lo = fast ? to_e4m3x2<true>(f[4 * j], f[4 * j + 1], sc, inv)
-                                   : to_e4m3x2<false>(f[4 * j], f[4 * j + 1], sc, inv);
-          const uint32_t hi = fast ? to_e4m3x2<true>(f[4 * j + 2], f[4 * j + 3], sc, inv)
-                                   : to_e4m3x2<false>(f[4 * j + 2], f[4 * j + 3], sc, inv);
-          o[j] = lo | (hi << 16);
+          for (int e = 0; e < VEC / 2; ++e) {
+            const float a = f[2 * e], b = f[2 * e + 1];
+            f[2 * e] = a * co[e] - b * s[e];
+            f[2 * e + 1] = a * s[e] + b * co[e];
+          }
         }
-        *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      } else {
-        *reinterpret_cast<uint4*>(dst) = pack<C>(f);
+        if (h < p.q_heads) {
+          *reinterpret_cast<uint4*>(q + h * p.head_dim) = pack<E>(f);
+          continue;
+        }
+        const int hk = hv >= 0 ? hv : h - p.q_heads;
+        C* dst = static_cast<C*>(hv >= 0 ? p.Vc : p.Kc) + slot + hk * p.page_size * static_cast<int64_t>(p.head_dim);
+        if constexpr (sizeof(C) == 1) {
+          const float sc = hv >= 0 ? sv : sk, inv = hv >= 0 ? inv_v : inv_k;
+          uint32_t o[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = fast ? to_e4m3x2<true>(f[4 * j], f[4 * j + 1], sc, inv)
+                                     : to_e4m3x2<false>(f[4 * j], f[4 * j + 1], sc, inv);
+            const uint32_t hi = fast ? to_e4m3x2<true>(f[4 * j + 2], f[4 * j + 3], sc, inv)
+                                     : to_e4m3x2<false>(f[4 * j + 2], f[4 * j + 3], sc, inv);
+            o[j] = lo | (hi << 16);
+          }
+          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+        } else {
+          *reinterpret_cast<uint4*>(dst) = pack<C>(f);
+        }
       }
     }
   }
@@ -1058,12 +1084,15 @@ cudaError_t pick_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
 
 }  // namespace
 
-cudaError_t launch_paged_append(const AppendParams& p, int64_t M, bool f32, bool e4m3, cudaStream_t s, bool pdl) {
+cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl) {
   const void* k = f32    ? reinterpret_cast<const void*>(append_kernel<float, float>)
                   : e4m3 ? reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_fp8_e4m3>)
                          : reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_bfloat16>);
+  // about the blocks that fit the GPU at once, each with its share of the rows
+  const int64_t fit = static_cast<int64_t>(device_sm_count()) * kAppendBlocks;
+  const int64_t turns = (p.M + fit - 1) / fit, grid = (p.M + turns - 1) / turns;
   void* args[] = {const_cast<AppendParams*>(&p)};
-  return launch_ex(k, dim3(static_cast<unsigned>(M)), dim3(kAppendThreads), 0, s, pdl, args);
+  return launch_ex(k, dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0, s, pdl, args);
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl) {
