@@ -91,7 +91,7 @@ __device__ __forceinline__ uint4 lifted(const uint4& w) {
 template <class E>
 __device__ __forceinline__ uint4 load_vec(const E* x, int v, int V) {
   constexpr int VEC = 16 / sizeof(E);
-  if ((v + 1) * VEC <= V) return __ldcs(reinterpret_cast<const uint4*>(x) + v);
+  if ((v + 1) * VEC <= V) return __ldg(reinterpret_cast<const uint4*>(x) + v);
   uint4 w;
   E* e = reinterpret_cast<E*>(&w);
 #pragma unroll
@@ -146,9 +146,9 @@ constexpr int kMaxCluster = 8;
 template <int NT>
 struct LogprobsShared {
   Sums warp[NT / 32];
-  uint32_t key[NT];       // each thread's largest value
-  int owner[NT];          // threads whose largest value reaches the bound
+  uint32_t tops[128];     // each warp's largest thread maxima
   uint32_t bound;
+  int owner[NT];          // threads whose largest value reaches the bound
   int owners, found;
   uint64_t cand[kCandidates];
   uint64_t red[NT / 32];
@@ -162,9 +162,9 @@ struct LogprobsShared {
 //
 // The alternatives cost the pass nothing: each thread knows its own largest
 // value, and the top-th largest of those is a bound that at least `top`
-// elements reach.  Only threads whose largest value reaches it can hold an
-// alternative (with distinct values `top` of them, each with 1 / NT of the
-// row), so their elements are read once more, from L2 as a rule: 20 of 512
+// elements reach (a slightly lower one is quicker to find).  Only threads whose
+// largest value reaches it can hold an alternative, each with 1 / NT of the
+// row, so their elements are read once more, from L2 as a rule: 20 of 512
 // threads are 4% of the row.  The few elements that reach the bound are ranked
 // by counting.  If ties leave more than kCandidates of them, the alternatives
 // are found one by one instead.
@@ -172,7 +172,7 @@ struct LogprobsShared {
 // Bound by the row's bytes.  bf16 costs about 5 issue slots an element (the
 // arithmetic is packed in pairs) of the 11 that the HBM rate leaves.
 template <class E, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+__global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   constexpr int VEC = 16 / sizeof(E), U = kRowVecs;
   __shared__ LogprobsShared<NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -184,22 +184,25 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   const int vecs = (p.V + VEC - 1) / VEC, per = (vecs + ranks - 1) / ranks;
   const int v0 = min(rank * per, vecs), v1 = min(v0 + per, vecs);
 
+  // the row's token: fetched now, its logit behind the loop, both used at the end
+  const int tgt = tid == 0 && rank == 0 ? p.targets[i] : -1;
+
   // This thread's running maximum m and sums relative to base = m log2 e, two of each side by side: d = x log2 e - base
   // is one operation for two elements.  -inf and huge negative logits are lifted to -2^126, whose weight is 0 as well.
   float m = -INFINITY, base = 0.0f;
   float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
   const int whole = min(v1, p.V / VEC);  // vectors without an end of the row inside
+  uint4 q[U];
   for (int v = v0 + tid; v < v1; v += U * NT) {
-    uint4 q[U];
     if (v + (U - 1) * NT < whole) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
+      for (int u = 0; u < U; ++u) q[u] = __ldg(reinterpret_cast<const uint4*>(x) + v + u * NT);
     } else {
       // the last round: what lies behind the row or this block's part of it is -inf
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (v + u * NT < whole)
-          q[u] = __ldcs(reinterpret_cast<const uint4*>(x) + v + u * NT);
+          q[u] = __ldg(reinterpret_cast<const uint4*>(x) + v + u * NT);
         else
           q[u] = load_vec<E>(x, v + u * NT < v1 ? v + u * NT : vecs, p.V);
       }
@@ -227,6 +230,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
       }
     }
   }
+  E at_tgt = {};
+  if (tgt >= 0 && tgt < p.V) at_tgt = x[tgt];
   // the sums relative to m itself: base was rounded by `off`
   Sums a = {m, s2.x + s2.y, t2.x + t2.y};
   if (!(m < INFINITY)) {
@@ -238,7 +243,18 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     a.t = (a.t - off * a.s) * c;
     a.s *= c;
   }
-  if (p.top > 0) sh.key[tid] = v0 + tid < v1 ? value_key(m) : 0u;
+  const uint32_t key = v0 + tid < v1 ? value_key(m) : 0u;
+  // The bound of the alternatives: each warp's `each` largest keys (taken out one by one), of all of those the top-th.
+  // top threads reach it, and with one or two more a warp than top needs few others do.
+  const int each = (p.top + NT / 32 - 1) / (NT / 32) + 1;
+  if (p.top > 0) {
+    uint32_t k = key;
+    for (int e = 0; e < each; ++e) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, k);
+      if (lane == 0) sh.tops[e * (NT / 32) + w] = best;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, k == best)) - 1) k = 0;
+    }
+  }
   if (tid == 0) {
     sh.owners = 0;
     sh.found = 0;
@@ -255,38 +271,35 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
       a.add(b);
     }
   };
-  auto block_sums = [&]() {  // into sh.part, by warp 0
+  warp_sums();
+  if (lane == 0) sh.warp[w] = a;
+  __syncthreads();
+  if (p.top > 0) {
+    // ranks by counting, a warp for each key; the lower place counts as larger among equals
+    const int n = each * (NT / 32);
+#pragma unroll 1
+    for (int c = w; c < n; c += NT / 32) {
+      const uint32_t mine = sh.tops[c];
+      int before = 0;
+#pragma unroll 1
+      for (int o = lane; o < ((n + 31) & ~31); o += 32) {
+        const uint32_t other = o < n ? sh.tops[o] : 0u;
+        before += __popc(__ballot_sync(0xffffffffu, o < n && (other > mine || (other == mine && o < c))));
+      }
+      if (before == p.top - 1) sh.bound = mine;  // one key has this rank
+    }
+  }
+  if (w == 0) {
+    a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
     warp_sums();
-    if (lane == 0) sh.warp[w] = a;
-    __syncthreads();
-    if (w == 0) {
-      a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
-      warp_sums();
-      if (lane == 0) sh.part = a;
-    }
-  };
-  block_sums();
-  if (w == 1 && p.top > 0) {
-    // the top-th largest of the threads' keys, bit by bit: bf16 keys differ in their upper 16 bits only
-    uint32_t k[NT / 32], bound = 0;
-#pragma unroll
-    for (int e = 0; e < NT / 32; ++e) k[e] = sh.key[lane + 32 * e];
-    for (int bit = 31; bit >= (sizeof(E) == 4 ? 0 : 16); --bit) {
-      const uint32_t t = bound | (1u << bit);
-      int c = 0;
-#pragma unroll
-      for (int e = 0; e < NT / 32; ++e) c += k[e] >= t;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c >= p.top) bound = t;
-      if (c == p.top) break;
-    }
-    if (lane == 0) sh.bound = bound;
+    if (lane == 0) sh.part = a;
   }
   __syncthreads();
-  if (fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY) {
+  if (__builtin_expect(fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
     // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
     const float top = sh.part.m;
     a = {top, 0.0f, 0.0f};
+#pragma unroll 1
     for (int v = v0 + tid; v < v1; v += NT) {
       float2 f[8 / sizeof(E)];
       pairs<E>(load_vec<E>(x, v, p.V), f);
@@ -297,8 +310,14 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
         a.t += g * d;
       }
     }
-    __syncthreads();  // every thread has read sh.part
-    block_sums();
+    warp_sums();
+    if (lane == 0) sh.warp[w] = a;
+    __syncthreads();  // and every thread has read sh.part
+    if (w == 0) {
+      a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+      warp_sums();
+      if (lane == 0) sh.part = a;
+    }
     __syncthreads();
   }
   int local = 0;  // alternatives this block has: min(top, its elements)
@@ -306,35 +325,47 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     const int64_t first = static_cast<int64_t>(v0) * VEC, last = min(static_cast<int64_t>(v1) * VEC, static_cast<int64_t>(p.V));
     local = static_cast<int>(min(static_cast<int64_t>(p.top), max(last - first, static_cast<int64_t>(0))));
     const uint32_t bound = sh.bound;
-    if (v0 + tid < v1 && sh.key[tid] >= bound) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
-    __syncthreads();
-    for (int o = w; o < sh.owners; o += NT / 32) {
-      for (int u = v0 + sh.owner[o] + lane * NT; u < v1; u += 32 * NT) {
-        const uint4 q = load_vec<E>(x, u, p.V);
-        const E* e = reinterpret_cast<const E*>(&q);
+    const bool owner = v0 + tid < v1 && key >= bound;
+    auto collect = [&](const uint4& vec, int u) {
+      const E* e = reinterpret_cast<const E*>(&vec);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const uint32_t j = u * VEC + k, key = value_key(to_f32(e[k]));
-          if (key >= bound && j < static_cast<uint32_t>(p.V)) {
-            const int at = atomicAdd(&sh.found, 1);
-            if (at < kCandidates) sh.cand[at] = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(~j);
-          }
+      for (int k = 0; k < VEC; ++k) {
+        const uint32_t j = u * VEC + k, val = value_key(to_f32(e[k]));
+        if (val >= bound && j < static_cast<uint32_t>(p.V)) {
+          const int at = atomicAdd(&sh.found, 1);
+          if (at < kCandidates) sh.cand[at] = (static_cast<uint64_t>(val) << 32) | static_cast<uint32_t>(~j);
         }
       }
+    };
+    if (CLUSTER && v1 - v0 <= U * NT) {  // one round of loads: an owner still has its elements
+      if (owner) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) collect(q[u], v0 + tid + u * NT < v1 ? v0 + tid + u * NT : vecs);
+      }
+    } else {
+      if (owner) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
+      __syncthreads();
+      for (int o = w; o < sh.owners; o += NT / 32)
+        for (int u = v0 + sh.owner[o] + lane * NT; u < v1; u += 32 * NT) collect(load_vec<E>(x, u, p.V), u);
     }
     __syncthreads();
     const int n = sh.found;
-    if (n <= kCandidates) {
-      for (int c = tid; c < n; c += NT) {
+    if (__builtin_expect(n <= kCandidates, 1)) {
+#pragma unroll 1
+      for (int c = w; c < n; c += NT / 32) {
         const uint64_t mine = sh.cand[c];
         int before = 0;
-        for (int o = 0; o < n; ++o) before += sh.cand[o] > mine;
+#pragma unroll 1
+        for (int o = lane; o < ((n + 31) & ~31); o += 32)
+          before += __popc(__ballot_sync(0xffffffffu, o < n && sh.cand[o] > mine));
         if (before < local) sh.best[before] = mine;
       }
     } else {
       uint64_t below = ~0ull;
+#pragma unroll 1
       for (int k = 0; k < local; ++k) {
         uint64_t best = 0;
+#pragma unroll 1
         for (int u = v0 + tid; u < v1; u += NT) {
           const uint4 q = load_vec<E>(x, u, p.V);
           const E* e = reinterpret_cast<const E*>(&q);
@@ -366,13 +397,16 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   if constexpr (CLUSTER) {
     cluster_sync();
     if (rank == 0) {
-      for (int r = 1; r < ranks; ++r) {
-        const uint32_t at = mapa_shared(smem_u32(&sh.part), r);
-        Sums b;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + 4) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.t) : "r"(at + 8) : "memory");
-        row.add(b);
+      if (w == 0) {  // a lane for each block
+        a = Sums{-INFINITY, 0.0f, 0.0f};
+        if (lane < ranks) {
+          const uint32_t at = mapa_shared(smem_u32(&sh.part), lane);
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.m) : "r"(at) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.s) : "r"(at + 4) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.t) : "r"(at + 8) : "memory");
+        }
+        warp_sums();
+        row = a;
       }
       // every block's alternatives side by side; a block with fewer has the key 0 in their place
       static_assert(kMaxCluster * kMaxTop <= kCandidates, "the cluster's alternatives fit the candidates");
@@ -388,41 +422,49 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
         sh.cand[c] = key;
       }
     }
-    cluster_sync();  // the other blocks' shared memory was read
-    if (rank != 0) return;
-    if (p.top > 0) {
-      __syncthreads();
-      const int n = ranks * p.top;
-      uint64_t keep[kMaxCluster * kMaxTop / NT + 1];
-      int before[kMaxCluster * kMaxTop / NT + 1];
-#pragma unroll
-      for (int e = 0; e < kMaxCluster * kMaxTop / NT + 1; ++e) {
-        const int c = tid + e * NT;
-        before[e] = p.top;
-        if (c < n) {
-          keep[e] = sh.cand[c];
-          before[e] = 0;
-          for (int o = 0; o < n; ++o) before[e] += sh.cand[o] > keep[e];
-          if (keep[e] == 0) before[e] = p.top;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kMaxCluster * kMaxTop / NT + 1; ++e)
-        if (before[e] < p.top) sh.best[before[e]] = keep[e];
-      __syncthreads();
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) {
+      cluster_wait();  // this block's shared memory was read
+      return;
     }
+    __syncthreads();
+    if (tid == 0) sh.part = row;
+    if (p.top > 0) {
+      // an alternative's rank: those above it in each block's list, found by bisection by a lane for each list (the
+      // lists' number is a power of two)
+      const int n = ranks * p.top * ranks;
+#pragma unroll 1
+      for (int c = tid; c < ((n + 31) & ~31); c += NT) {
+        const int from = min(c, n - 1);
+        const uint64_t mine = sh.cand[from / ranks];
+        const uint64_t* list = sh.cand + (from & (ranks - 1)) * p.top;
+        int lo = 0, hi = p.top;
+#pragma unroll 1
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (list[mid] > mine)
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        for (int o = 1; o < ranks; o <<= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        if (c < n && (c & (ranks - 1)) == 0 && lo < p.top && mine != 0) sh.best[lo] = mine;
+      }
+    }
+    __syncthreads();
+    row = sh.part;
   }
 
   // ---- results
   const bool empty = row.s == 0.0f;  // nothing but -inf
   const float log_s = logf(row.s);
   if (tid == 0) {
-    const int tgt = p.targets[i];
     float lp = 0.0f;
     if (tgt >= p.V)
       atomicOr(&g_logprobs_status, kDevBadIndex);
     else if (tgt >= 0)
-      lp = empty ? -INFINITY : (to_f32(x[tgt]) - row.m) - log_s;
+      lp = empty ? -INFINITY : (to_f32(at_tgt) - row.m) - log_s;
     p.logp[i] = lp;
     if (p.entropy) p.entropy[i] = empty ? 0.0f : log_s - row.t / row.s * kLn2;
     if (p.lse) p.lse[i] = empty ? -INFINITY : row.m + log_s;
@@ -431,6 +473,10 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     const uint64_t key = sh.best[k];
     p.top_ids[i * p.top + k] = static_cast<int>(~static_cast<uint32_t>(key));
     p.top_logp[i * p.top + k] = empty ? -INFINITY : (key_value(static_cast<uint32_t>(key >> 32)) - row.m) - log_s;
+  }
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    cluster_wait();
   }
 }
 
