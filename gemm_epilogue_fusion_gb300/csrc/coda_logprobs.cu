@@ -129,14 +129,6 @@ struct Sums {
     }
     m = mn;
   }
-  __device__ __forceinline__ void add(const Sums& o) {
-    const float mn = max_nan(m, o.m);
-    Sums b = o;
-    raise(mn);
-    b.raise(mn);
-    s += b.s;
-    t += b.t;
-  }
 };
 
 constexpr int kRowThreads = 512, kRowVecs = 4;  // threads of a block, vectors of a thread in flight
@@ -244,39 +236,32 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
     a.s *= c;
   }
   const uint32_t key = v0 + tid < v1 ? value_key(m) : 0u;
-  // The bound of the alternatives: each warp's `each` largest keys (taken out one by one), of all of those the top-th.
-  // top threads reach it, and with one or two more a warp than top needs few others do.
-  const int each = (p.top + NT / 32 - 1) / (NT / 32) + 1;
+  if (tid == 0) {
+    sh.owners = 0;
+    sh.found = 0;
+  }
+  // sums of a warp relative to its largest m
+  auto warp_sums = [&]() {
+    a.raise(key_value(__reduce_max_sync(0xffffffffu, value_key(a.m))));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+      a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
+    }
+  };
+
+  // ---- the bound of the alternatives: each warp's `each` largest keys (taken out one by one), of all of those the
+  // top-th.  top threads reach it, and with one or two more a warp than top needs few others do.
   if (p.top > 0) {
+    const int each = (p.top + NT / 32 - 1) / (NT / 32) + 1, n = each * (NT / 32);
     uint32_t k = key;
     for (int e = 0; e < each; ++e) {
       const uint32_t best = __reduce_max_sync(0xffffffffu, k);
       if (lane == 0) sh.tops[e * (NT / 32) + w] = best;
       if (lane == __ffs(__ballot_sync(0xffffffffu, k == best)) - 1) k = 0;
     }
-  }
-  if (tid == 0) {
-    sh.owners = 0;
-    sh.found = 0;
-  }
-
-  // ---- the row's sums
-  auto warp_sums = [&]() {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Sums b;
-      b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-      b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-      b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
-      a.add(b);
-    }
-  };
-  warp_sums();
-  if (lane == 0) sh.warp[w] = a;
-  __syncthreads();
-  if (p.top > 0) {
+    __syncthreads();
     // ranks by counting, a warp for each key; the lower place counts as larger among equals
-    const int n = each * (NT / 32);
 #pragma unroll 1
     for (int c = w; c < n; c += NT / 32) {
       const uint32_t mine = sh.tops[c];
@@ -288,39 +273,11 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
       }
       if (before == p.top - 1) sh.bound = mine;  // one key has this rank
     }
-  }
-  if (w == 0) {
-    a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
-    warp_sums();
-    if (lane == 0) sh.part = a;
-  }
-  __syncthreads();
-  if (__builtin_expect(fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
-    // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
-    const float top = sh.part.m;
-    a = {top, 0.0f, 0.0f};
-#pragma unroll 1
-    for (int v = v0 + tid; v < v1; v += NT) {
-      float2 f[8 / sizeof(E)];
-      pairs<E>(load_vec<E>(x, v, p.V), f);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = fmaxf(((e & 1 ? f[e / 2].y : f[e / 2].x) - top) * kLog2e, -200.0f), g = ex2_approx(d);
-        a.s += g;
-        a.t += g * d;
-      }
-    }
-    warp_sums();
-    if (lane == 0) sh.warp[w] = a;
-    __syncthreads();  // and every thread has read sh.part
-    if (w == 0) {
-      a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
-      warp_sums();
-      if (lane == 0) sh.part = a;
-    }
     __syncthreads();
   }
+  // ---- the elements that reach it, and the row's sums meanwhile
   int local = 0;  // alternatives this block has: min(top, its elements)
+  bool sums_done = false;
   if (p.top > 0) {
     const int64_t first = static_cast<int64_t>(v0) * VEC, last = min(static_cast<int64_t>(v1) * VEC, static_cast<int64_t>(p.V));
     local = static_cast<int>(min(static_cast<int64_t>(p.top), max(last - first, static_cast<int64_t>(0))));
@@ -345,10 +302,26 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
     } else {
       if (owner) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
       __syncthreads();
-      for (int o = w; o < sh.owners; o += NT / 32)
+      const int owners = sh.owners, u0 = w < owners ? v0 + sh.owner[w] + lane * NT : v1;
+      uint4 vec;
+      if (u0 < v1) vec = load_vec<E>(x, u0, p.V);
+      warp_sums();  // while the first owner's elements are on their way
+      sums_done = true;
+      if (u0 < v1) collect(vec, u0);
+      for (int u = u0 + 32 * NT; u < v1; u += 32 * NT) collect(load_vec<E>(x, u, p.V), u);
+      for (int o = w + NT / 32; o < owners; o += NT / 32)
         for (int u = v0 + sh.owner[o] + lane * NT; u < v1; u += 32 * NT) collect(load_vec<E>(x, u, p.V), u);
     }
-    __syncthreads();
+  }
+  if (!sums_done) warp_sums();
+  if (lane == 0) sh.warp[w] = a;
+  __syncthreads();
+  if (w == 0) {
+    a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+    warp_sums();
+    if (lane == 0) sh.part = a;
+  }
+  if (p.top > 0) {
     const int n = sh.found;
     if (__builtin_expect(n <= kCandidates, 1)) {
 #pragma unroll 1
@@ -391,6 +364,31 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
     }
   }
   __syncthreads();
+  if (__builtin_expect(fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
+    // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
+    const float top = sh.part.m;
+    a = {top, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int v = v0 + tid; v < v1; v += NT) {
+      float2 f[8 / sizeof(E)];
+      pairs<E>(load_vec<E>(x, v, p.V), f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = fmaxf(((e & 1 ? f[e / 2].y : f[e / 2].x) - top) * kLog2e, -200.0f), g = ex2_approx(d);
+        a.s += g;
+        a.t += g * d;
+      }
+    }
+    warp_sums();
+    if (lane == 0) sh.warp[w] = a;
+    __syncthreads();  // and every thread has read sh.part
+    if (w == 0) {
+      a = lane < NT / 32 ? sh.warp[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+      warp_sums();
+      if (lane == 0) sh.part = a;
+    }
+    __syncthreads();
+  }
 
   // ---- the cluster's parts, collected by its first block
   Sums row = sh.part;
@@ -406,7 +404,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a.t) : "r"(at + 8) : "memory");
         }
         warp_sums();
-        row = a;
+        row = a;  // lane 0's is handed on below
       }
       // every block's alternatives side by side; a block with fewer has the key 0 in their place
       static_assert(kMaxCluster * kMaxTop <= kCandidates, "the cluster's alternatives fit the candidates");
@@ -458,7 +456,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
 
   // ---- results
   const bool empty = row.s == 0.0f;  // nothing but -inf
-  const float log_s = logf(row.s);
+  const float log_s = tid == 0 || tid < p.top ? logf(row.s) : 0.0f;
   if (tid == 0) {
     float lp = 0.0f;
     if (tgt >= p.V)
