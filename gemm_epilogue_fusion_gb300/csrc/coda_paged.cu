@@ -217,7 +217,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 
 // What a block does with a key/value head's query heads at a time:
-//   kFew   up to 4 (fp32: 1);  kSome  up to 8;  kMany  up to 16 (fp32: 8)
+//   kFew   up to 4 (fp32: 1);  kSome  up to 8 (fp32: 4);  kMany  up to 16 (fp32: 8)
 enum Heads { kFew, kSome, kMany };
 
 template <class T, class C, int DP_, Heads HEADS_>
@@ -227,21 +227,23 @@ struct AttnShape {
   static constexpr Heads HEADS = HEADS_;
   static constexpr int DP = DP_;                              // head_dim rounded up
   static constexpr int NH = HEADS == kMany ? 2 : 1;           // mma: tiles of 8 heads
-  static constexpr int RG = F32 ? (HEADS == kFew ? 1 : 8) : 8 * NH;   // rows of state
+  static constexpr int RG = F32 ? (HEADS == kFew ? 1 : HEADS == kSome ? 4 : 8) : 8 * NH;   // rows of state
   static constexpr int MAXG = F32 ? RG : HEADS == kFew ? 4 : RG;      // query heads of a block
   static constexpr int PITCH = DP * static_cast<int>(sizeof(C));      // bytes of a staged row
   static constexpr int KT0 = 4096 / PITCH;
-  static constexpr int KT = F32 ? (DP == 256 ? 8 : 16) : KT0 < 16 ? 16 : KT0 > 32 ? 32 : KT0;  // keys of a warp's tile
+  static constexpr int KT = F32 ? 1024 / DP : KT0 < 16 ? 16 : KT0 > 32 ? 32 : KT0;  // keys of a warp's tile
   static constexpr int CT = KT * kAttnWarps;
-  static constexpr int ST = 2;
   static constexpr int STAGE = 2 * KT * PITCH;
+  static constexpr int ST = STAGE <= 4096 ? 4 : 2;  // about 64 KB in a block's ring
   static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
   static constexpr int RING = kAttnWarps * ST * STAGE;
   static constexpr int OS = DP + 4;  // floats between the rows of a join buffer
   static constexpr int JOIN = 2 * RG * OS * 4;
-  static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : 0;
+  // the widest shape keeps its queries in shared memory: 64 registers a thread that o needs
+  static constexpr bool Q_SMEM = !F32 && NH == 2 && DP == 256;
+  static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : Q_SMEM ? DP / 16 * 32 * 16 : 0;
   static constexpr int SMEM = RING + JOIN + QBYTES;
-  static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + DP / 8) + 72;  // about what a thread needs
+  static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + (Q_SMEM ? 0 : DP / 8)) + 72;  // about what a thread needs
   static constexpr int BY_SMEM = 233472 / (SMEM + 1024 + 640), BY_REGS = 65536 / (kAttnThreads * REGS);
   static constexpr int CTAS0 = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
   static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > 3 ? 3 : CTAS0;  // blocks on an SM
@@ -516,6 +518,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   const char* const k_src = static_cast<const char*>(p.Kc) + (lane % LPR) * 16;
   const char* const v_src = static_cast<const char*>(p.Vc) + (lane % LPR) * 16;
   auto issue = [&](int stage) {
+    if (in.t == 0 && w == 0) {
+      // a new item: its queries start their way to L2 (the products need them as soon as these keys are there)
+      const int g0 = (in.h % groups) * gsize, bytes = min(gsize, G - g0) * p.head_dim * static_cast<int>(sizeof(E));
+      const char* src = reinterpret_cast<const char*>(static_cast<const E*>(p.Q) + in.row * p.ldq +
+                                                      static_cast<int64_t>(in.h / groups * G + g0) * p.head_dim);
+      for (int b = lane * 128; b < bytes; b += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b));
+    }
     const bool ok = pg >= 0 && pg < p.num_pages && slot >= 0;
     bad_page |= !ok && slot >= 0;
     // row of the caches (fewer than 2^31); -1: filled with zeros
@@ -564,6 +573,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)
   float* s_q = reinterpret_cast<float*>(smem + S::RING + S::JOIN);  // fp32: [RG][DP]
   float* s_p = s_q + RG * DP + w * KT * RG;                         // fp32: [KT][RG] of this warp
+  uint4* s_frag = reinterpret_cast<uint4*>(s_q);                    // Q_SMEM: [KS][32]
   const float sk = S::E4M3 ? p.scale * *p.scale_k : p.scale;
   const float sv = S::E4M3 ? *p.scale_v : 1.0f;
 
@@ -621,6 +631,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
           for (int x = 0; x < 2; ++x) s2[2 * nh + x] = __shfl_sync(0xffffffffu, down, (2 * c4 + x) * 4);
         }
       }
+      if constexpr (S::Q_SMEM) {
+        // every warp has the same fragments: one writes them, [step][lane] of both heads' tiles
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            s_frag[ks * 32 + lane] = make_uint4(q[ks * 2], q[ks * 2 + 1], q[(KS + ks) * 2], q[(KS + ks) * 2 + 1]);
+        }
+        __syncthreads();
+      }
     }
   };
 
@@ -629,6 +649,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     constexpr int MT = KT < 16 ? 1 : KT / 16;
     const uint32_t kb = ring + stage * S::STAGE, vb = kb + KT * PITCH;
     // s^T = k q^T: 16 keys by 8 heads a tile
+    auto query = [&](int ks, uint32_t (&b)[2 * NH]) {
+      if constexpr (S::Q_SMEM) {
+        const uint4 v = s_frag[ks * 32 + lane];
+        b[0] = v.x;
+        b[1] = v.y;
+        b[2 * NH - 2] = v.z;
+        b[2 * NH - 1] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * NH; ++i) b[i] = q[((i >> 1) * KS + ks) * 2 + (i & 1)];
+      }
+    };
     float s[NH][MT][4];
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
@@ -642,11 +674,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       if constexpr (!S::E4M3) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t a[4];
+          uint32_t a[4], b[2 * NH];
           ldmatrix4<false>(a, kb + staged<PITCH>(row, ks * 2 + (lane >> 4)));
+          query(ks, b);
 #pragma unroll
-          for (int nh = 0; nh < NH; ++nh)
-            mma16816<F16>(s[nh][t], a[0], a[1], a[2], a[3], q[(nh * KS + ks) * 2], q[(nh * KS + ks) * 2 + 1]);
+          for (int nh = 0; nh < NH; ++nh) mma16816<F16>(s[nh][t], a[0], a[1], a[2], a[3], b[2 * nh], b[2 * nh + 1]);
         }
       } else {
         // a lane's 4 bytes are 4 consecutive columns: the pairs (0, 1) and (2, 3) are taken as the instruction's
@@ -659,9 +691,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
           for (int u = 0; u < 2; ++u) {
             const uint32_t a0 = e4m3x2_f16x2(a[2 * u]), a1 = e4m3x2_f16x2(a[2 * u + 1]);
             const uint32_t a2 = e4m3x2_f16x2_hi(a[2 * u]), a3 = e4m3x2_f16x2_hi(a[2 * u + 1]);
+            uint32_t b[2 * NH];
+            query(ks + u, b);
 #pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-              mma16816<F16>(s[nh][t], a0, a1, a2, a3, q[(nh * KS + ks + u) * 2], q[(nh * KS + ks + u) * 2 + 1]);
+            for (int nh = 0; nh < NH; ++nh) mma16816<F16>(s[nh][t], a0, a1, a2, a3, b[2 * nh], b[2 * nh + 1]);
           }
         }
       }
@@ -777,20 +810,23 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     const uint8_t* vb = kb + KT * PITCH;
     const int key = lane % KT, part = lane / KT;
     float s[RG];
+    float2 s2v[RG];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) s[g] = 0.0f;
+    for (int g = 0; g < RG; ++g) s2v[g] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
     for (int c = part; c < CPR; c += PARTS) {
       const float4 k = *reinterpret_cast<const float4*>(kb + staged<PITCH>(key, c));
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
         const float4 x = *reinterpret_cast<const float4*>(s_q + g * DP + 4 * c);
-        s[g] += (k.x * x.x + k.y * x.y) + (k.z * x.z + k.w * x.w);
+        s2v[g] = ffma2(make_float2(k.x, k.y), make_float2(x.x, x.y), s2v[g]);
+        s2v[g] = ffma2(make_float2(k.z, k.w), make_float2(x.z, x.w), s2v[g]);
       }
     }
     const bool there = (mask >> key) & 1u;
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
+      s[g] = s2v[g].x + s2v[g].y;
 #pragma unroll
       for (int x = KT; x < 32; x <<= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], x);
       s[g] = there ? s[g] * s2[g] : -INFINITY;
@@ -832,7 +868,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       for (int g = 0; g < RG; ++g) {
         const float pr = s_p[t * RG + g];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) o[g * NC + i] += pr * v[i];
+        for (int i = 0; i < NC; i += 2) {
+          const float2 r = ffma2(make_float2(pr, pr), make_float2(v[i], v[i + 1]),
+                                 make_float2(o[g * NC + i], o[g * NC + i + 1]));
+          o[g * NC + i] = r.x;
+          o[g * NC + i + 1] = r.y;
+        }
       }
     }
     __syncwarp();
@@ -1074,7 +1115,8 @@ template <class T, class C>
 cudaError_t pick_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
   const int G = p.q_heads / p.kv_heads;
   if constexpr (sizeof(T) == 4) {
-    return G == 1 ? pick_width<T, C, kFew>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
+    if (G == 1) return pick_width<T, C, kFew>(p, s, pdl);
+    return G <= 4 ? pick_width<T, C, kSome>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
   } else {
     if constexpr (sizeof(C) == 2)  // f16 weights need no second part: kFew is for bf16
       if (G <= 4) return pick_width<T, C, kFew>(p, s, pdl);
