@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
 // gradient.  A block takes kGradVecs vectors a thread of one row, so the row's
 // statistics are read once for 16 KB and the loads are in flight meanwhile.
 //   dx = 2^(lp log2 e) (A + B lp),  lp = x - lse, A = -(dlogp + dH H), B = -dH
-constexpr int kGradThreads = 256, kGradVecs = 4;
+constexpr int kGradThreads = 128, kGradVecs = 4;
 
 template <class E>
 __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const __grid_constant__ LogprobsGradParams p) {

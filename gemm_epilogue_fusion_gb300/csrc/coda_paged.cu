@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- attention ----
-// One new token per row, flash-decoding style: o = sum_t p_t v_t / sum_t p_t,
+// One new token per row: o = sum_t p_t v_t / sum_t p_t,
 // p_t = 2^(s_t - m), with the running maximum m, the sum and o kept in fp32 and
 // every key and value read once.
 //
@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     const int r0 = min(tid * per, p.M), r1 = min(r0 + per, p.M);
     int64_t sum = 0;
     bool bad = false;
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) sum += max(1, (row_info(p, r, bad).len + CT - 1) / CT);
     if (bad && blockIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
     int64_t incl = sum;

@@ -190,7 +190,7 @@ def check(q, k, v, table, lens, s, got_o, got_lse, row_seq=None, scale=None):
 
 
 HEADS = [(32, 8, 128, 16), (64, 8, 128, 64), (4, 4, 64, 5), (16, 1, 80, 24), (14, 2, 256, 1), (40, 2, 96, 128),
-         (1, 1, 16, 3), (9, 1, 48, 7), (6, 3, 192, 16), (34, 1, 64, 16)]
+         (1, 1, 16, 3), (9, 1, 48, 7), (6, 3, 192, 16), (34, 1, 64, 16), (16, 1, 256, 16), (5, 1, 128, 2), (8, 2, 256, 8)]
 
 
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
@@ -208,6 +208,54 @@ def test_attention_against_64_bits(types, hq, hkv, d, page):
     check(q, k, v, table, ln, s, o, lse)
     again = gg.coda_paged_attention(*args, **kw)  # the workspace is ready for the next call, and the bits are the same
     assert torch.equal(o, again)
+
+
+@pytest.mark.parametrize("types,d", [((BF, BF), 8), ((F32, F32), 4), ((F32, F32), 12)], ids=["bf16-8", "f32-4", "f32-12"])
+def test_attention_and_append_of_the_narrowest_heads(types, d):
+    import gemm_epilogue_fusion_gb300 as gg
+    hq, hkv, page, lens = 3, 3, 4, [1, 0, 30, 65]
+    q, k, v, table, ln, s = make(hq, hkv, d, page, lens, types, d)
+    ws = gg.paged_attention_workspace(hq, hkv, d, "cuda")
+    lse = torch.empty(4, hq).cuda()
+    kc, vc = k.cuda(), v.cuda()
+    o = gg.coda_paged_attention(q.cuda(), kc, vc, table.cuda(), ln.cuda(), ws, lse=lse)
+    check(q, k, v, table, ln, s, o, lse)
+    Z = randn(4, 3 * hq * d, dtype=types[0], g=U.gen(1))
+    pos = torch.tensor([0, -1, 29, 64], dtype=torch.int32)
+    gg.coda_paged_append(Z.cuda(), pos.cuda(), table.cuda(), kc, vc, hq, want_q=False)
+    for i, p in ((0, 0), (2, 29), (3, 64)):
+        assert torch.equal(kc[table[i, p // page], :, p % page].cpu(), Z[i, hq * d:2 * hq * d].view(hkv, d))
+        assert torch.equal(vc[table[i, p // page], :, p % page].cpu(), Z[i, 2 * hq * d:].view(hkv, d))
+    assert gg.coda_get_device_status() == gg.CODA_OK
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+def test_attention_does_not_mix_rows_in_a_long_batch(types):
+    """Thousands of short rows: one key each, so every output is that key's value, and rows without keys between them."""
+    import gemm_epilogue_fusion_gb300 as gg
+    hq, hkv, d, page, M = 4, 2, 64, 4, 5003
+    lens = [(1 if i % 7 else 0) for i in range(M)]
+    q, k, v, table, ln, s = make(hq, hkv, d, page, lens, types, 77)
+    ws = gg.paged_attention_workspace(hq, hkv, d, "cuda")
+    o = gg.coda_paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ln.cuda(), ws, **scales(types[1], s)).cpu()
+    first = v.view(torch.uint8 if types[1] == E4 else types[1])[table[:, 0].clamp(min=0).long(), :, 0]
+    first = (first.view(E4) if types[1] == E4 else first).to(U.F64) * s[1]
+    want = first[:, :, None].expand(M, hkv, hq // hkv, d).reshape(M, hq * d) * (ln > 0).to(U.F64)[:, None]
+    # a single weight of 1: the scale's product and the output's rounding are left
+    assert ((o.to(U.F64) - want).abs() <= (U.HALF[types[0]] + 2.0 ** -21) * want.abs()).all()
+
+
+def test_attention_workspace_serves_other_heads_and_batches():
+    """One workspace, sized for the larger heads, taken in turn by calls of other shapes: every call leaves it ready."""
+    import gemm_epilogue_fusion_gb300 as gg
+    shapes = [(32, 8, 128, 16, [3000, 5]), (4, 2, 64, 16, [9000]), (8, 8, 128, 5, [100] * 20), (32, 8, 128, 16, [1])]
+    ws = gg.paged_attention_workspace(32, 8, 128, "cuda")
+    for _ in range(2):
+        for hq, hkv, d, page, lens in shapes:
+            q, k, v, table, ln, s = make(hq, hkv, d, page, lens, (BF, BF), hq + d)
+            fresh = gg.paged_attention_workspace(hq, hkv, d, "cuda")
+            args = (q.cuda(), k.cuda(), v.cuda(), table.cuda(), ln.cuda())
+            assert torch.equal(gg.coda_paged_attention(*args, ws), gg.coda_paged_attention(*args, fresh))
 
 
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
