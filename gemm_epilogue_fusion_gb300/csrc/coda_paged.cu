@@ -231,22 +231,21 @@ struct AttnShape {
   static constexpr int MAXG = F32 ? RG : HEADS == kFew ? 4 : RG;      // query heads of a block
   static constexpr int PITCH = DP * static_cast<int>(sizeof(C));      // bytes of a staged row
   static constexpr int KT0 = 4096 / PITCH;
-  static constexpr int KT = F32 ? 1024 / DP : KT0 < 16 ? 16 : KT0 > 32 ? 32 : KT0;  // keys of a warp's tile
+  static constexpr int KT = F32 ? 1024 / DP : KT0 > 32 || (E4M3 && NH == 2) ? 32 : KT0 < 16 ? 16 : KT0;  // keys of a warp's tile
   static constexpr int CT = KT * kAttnWarps;
   static constexpr int STAGE = 2 * KT * PITCH;
   static constexpr int ST = STAGE <= 4096 ? 4 : 2;  // about 64 KB in a block's ring
   static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
   static constexpr int RING = kAttnWarps * ST * STAGE;
-  static constexpr int OS = DP + 4;  // floats between the rows of a join buffer
-  static constexpr int JOIN = 2 * RG * OS * 4;
   // the widest shape keeps its queries in shared memory: 64 registers a thread that o needs
   static constexpr bool Q_SMEM = !F32 && NH == 2 && DP == 256;
   static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : Q_SMEM ? DP / 16 * 32 * 16 : 0;
-  static constexpr int SMEM = RING + JOIN + QBYTES;
-  static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + (Q_SMEM ? 0 : DP / 8)) + 72;  // about what a thread needs
-  static constexpr int BY_SMEM = 233472 / (SMEM + 1024 + 640), BY_REGS = 65536 / (kAttnThreads * REGS);
+  static constexpr int SMEM = RING + QBYTES;
+  static_assert(RG * DP * 4 <= STAGE, "a warp's part of o fits a stage of its ring");
+  static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + (Q_SMEM ? 0 : DP / 8)) + 80;  // about what a thread needs
+  static constexpr int BY_SMEM = 233472 / (SMEM + 1024 + 1024), BY_REGS = 65536 / (kAttnThreads * REGS);
   static constexpr int CTAS0 = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
-  static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > 3 ? 3 : CTAS0;  // blocks on an SM
+  static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > (NH == 2 && DP > 64 ? 2 : 3) ? (NH == 2 && DP > 64 ? 2 : 3) : CTAS0;  // blocks on an SM
 };
 
 // Chunk c of staged row `row`: 16-byte chunks are permuted within 128 bytes so
@@ -429,14 +428,13 @@ template <class E, class C, int DP, Heads HEADS>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
   using S = AttnShape<E, C, DP, HEADS>;
-  constexpr int KT = S::KT, CT = S::CT, ST = S::ST, PITCH = S::PITCH, CPR = S::CPR, RG = S::RG, NH = S::NH, OS = S::OS;
+  constexpr int KT = S::KT, CT = S::CT, ST = S::ST, PITCH = S::PITCH, CPR = S::CPR, RG = S::RG, NH = S::NH;
   constexpr bool F16 = S::E4M3;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kAttnWarps];
   __shared__ int s_start[3], s_last;
   __shared__ uint32_t s_mask[kAttnWarps][ST];
-  __shared__ float s_ml[2][RG][2];
-  float* s_o = reinterpret_cast<float*>(smem + S::RING);  // [2][RG][OS]
+  __shared__ float2 s_ml[kAttnWarps][RG];  // (m, l) of the warps' parts of an item
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int G = p.q_heads / p.kv_heads, groups = (G + S::MAXG - 1) / S::MAXG, gsize = (G + groups - 1) / groups;
   const int units = p.kv_heads * groups;
@@ -572,7 +570,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   float o[OW], m[NR], l[NR];
   uint32_t q[S::F32 ? 1 : NH * KS * 2] = {};
   float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)
-  float* s_q = reinterpret_cast<float*>(smem + S::RING + S::JOIN);  // fp32: [RG][DP]
+  float* s_q = reinterpret_cast<float*>(smem + S::RING);  // fp32: [RG][DP]
   float* s_p = s_q + RG * DP + w * KT * RG;                         // fp32: [KT][RG] of this warp
   uint4* s_frag = reinterpret_cast<uint4*>(s_q);                    // Q_SMEM: [KS][32]
   const float sk = S::E4M3 ? p.scale * *p.scale_k : p.scale;
@@ -880,47 +878,37 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     __syncwarp();
   };
 
-  // This lane's elements of o: f(row, column, value index); and the row of state r.
-  auto each = [&](auto&& f) {
+  // o of a warp's part of an item lies in the stage of its ring that was just used up: element (row, d) at
+  // [row][d ^ 8 (row / 2 mod 4)], so that the four lanes of two rows each write to different banks.
+  auto part_at = [&](int warp, int st, int row, int d) {
+    return reinterpret_cast<float*>(smem + (warp * ST + st) * S::STAGE) + row * DP + (d ^ ((row & 6) << 2));
+  };
+  auto put = [&](int st) {
     if constexpr (S::F32) {
       constexpr int NC = DP / 32;
 #pragma unroll
-      for (int g = 0; g < RG; ++g)
+      for (int g = 0; g < RG; ++g) {
+        if (lane == 0) s_ml[w][g] = make_float2(m[g], l[g]);
+        if constexpr (NC == 2) {
+          *reinterpret_cast<float2*>(part_at(w, st, g, 2 * lane)) = make_float2(o[g * 2], o[g * 2 + 1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) f(g, NC == 2 ? 2 * lane + i : 4 * lane + 128 * (i / 4) + i % 4, g * NC + i);
-    } else {
+          for (int i = 0; i < NC; i += 4)
+            *reinterpret_cast<float4*>(part_at(w, st, g, 4 * lane + 32 * i)) =
+                make_float4(o[g * NC + i], o[g * NC + i + 1], o[g * NC + i + 2], o[g * NC + i + 3]);
+        }
+      }
+    } else if (!LOW_COLS || (lane & 2) == 0) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        if (lane < 4) s_ml[w][(r >> 1) * 8 + 2 * lane + (r & 1)] = make_float2(m[r], l[r]);
 #pragma unroll
       for (int i = 0; i < OW; ++i) {
         const int nh = i / (DP / 4), d = i % (DP / 4) / 4 * 16, hf = (i >> 1) & 1;
-        f(nh * 8 + 2 * (lane & 3) + (i & 1), d + (S::E4M3 ? 2 * (lane >> 2) + hf : 8 * hf + (lane >> 2)), i);
+        *part_at(w, st, nh * 8 + 2 * (lane & 3) + (i & 1), d + (S::E4M3 ? 2 * (lane >> 2) + hf : 8 * hf + (lane >> 2))) =
+            o[i];
       }
     }
-  };
-  auto row_of = [&](int r) { return S::F32 ? r : (r >> 1) * 8 + 2 * (lane & 3) + (r & 1); };
-  // (m, l, o) of this warp into or out of join buffer b
-  auto put = [&](int b) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-      if (lane < (S::F32 ? 1 : 4)) {
-        s_ml[b][row_of(r)][0] = m[r];
-        s_ml[b][row_of(r)][1] = l[r];
-      }
-    each([&](int row, int d, int i) { s_o[(b * RG + row) * OS + d] = o[i]; });
-  };
-  auto take = [&](int b) {
-    float c[NR], c2[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float m2 = s_ml[b][row_of(r)][0], mn = fmaxf(m[r], m2), base = mn == -INFINITY ? 0.0f : mn;
-      c[r] = ex2_approx(m[r] - base);
-      c2[r] = ex2_approx(m2 - base);
-      m[r] = mn;
-      l[r] = l[r] * c[r] + s_ml[b][row_of(r)][1] * c2[r];
-    }
-    each([&](int row, int d, int i) {
-      const int r = S::F32 ? i / (DP / 32) : i / (DP / 4) * 2 + (i & 1);
-      o[i] = o[i] * c[r] + s_o[(b * RG + row) * OS + d] * c2[r];
-    });
   };
 
   // Counters [2][kMaxWorkers], then per block two parts of (m, l) [gsize] and o [gsize][head_dim]
@@ -946,8 +934,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     if (p.lse && d == 0) p.lse[head] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
   };
 
-  // The warps' parts of tiles [first, i] of the item at `at` joined, and written out or left for the last block.
-  auto end_item = [&](int64_t first_tile, int64_t last_tile) {  // of the whole item, among all T
+  // The warps' parts of the item at `at` joined, and written out or left for the last block.  first_tile, last_tile: of
+  // the whole item, among all T; st: the stage that was just used up.
+  auto end_item = [&](int64_t first_tile, int64_t last_tile, int st) {
     if constexpr (!S::F32) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
@@ -964,25 +953,34 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         for (int x = 16; x > 0; x >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], x);
     }
     const int ng = min(gsize, G - (at.h % groups) * gsize), vecs = p.head_dim / 4;
-    if (w >= 2) put(w - 2);
-    __syncthreads();
-    if (w < 2) take(w);
-    __syncthreads();
-    if (w < 2) put(w);
+    __syncwarp();  // every lane has read this stage
+    put(st);
     __syncthreads();
     auto both = [&](int r, int d, float& mm, float& ll) {
-      const float m0 = s_ml[0][r][0], m1 = s_ml[1][r][0];
-      mm = fmaxf(m0, m1);
-      const float base = mm == -INFINITY ? 0.0f : mm, c0 = ex2_approx(m0 - base), c1 = ex2_approx(m1 - base);
-      ll = s_ml[0][r][1] * c0 + s_ml[1][r][1] * c1;
-      const float4 a = *reinterpret_cast<const float4*>(s_o + r * OS + d);
-      const float4 b = *reinterpret_cast<const float4*>(s_o + (RG + r) * OS + d);
-      return make_float4(a.x * c0 + b.x * c1, a.y * c0 + b.y * c1, a.z * c0 + b.z * c1, a.w * c0 + b.w * c1);
+      float2 ml[kAttnWarps];
+      mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kAttnWarps; ++x) {
+        ml[x] = s_ml[x][r];
+        mm = fmaxf(mm, ml[x].x);
+      }
+      const float base = mm == -INFINITY ? 0.0f : mm;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ll = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kAttnWarps; ++x) {
+        const float c = ex2_approx(ml[x].x - base);
+        const float4 a = *reinterpret_cast<const float4*>(part_at(x, st, r, d));
+        ll += ml[x].y * c;
+        v = make_float4(v.x + a.x * c, v.y + a.y * c, v.z + a.z * c, v.w + a.w * c);
+      }
+      return v;
     };
+    auto row_of = [&](int i) { return p.head_dim == DP ? i / (DP / 4) : i / vecs; };
     const bool whole = first_tile >= i0 && last_tile < i1;
     if (whole) {
       for (int i = tid; i < ng * vecs; i += kAttnThreads) {
-        const int r = i / vecs, d = (i % vecs) * 4;
+        const int r = row_of(i), d = (i - r * vecs) * 4;
         float mm, ll;
         const float4 v = both(r, d, mm, ll);
         write_row(r, d, v, mm, ll);
@@ -994,7 +992,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       auto part_of = [&](int c) { return parts + (2 * c + (c == wf ? second : 0)) * static_cast<int64_t>(part_floats); };
       float* mine = part_of(blockIdx.x);
       for (int i = tid; i < ng * vecs; i += kAttnThreads) {
-        const int r = i / vecs, d = (i % vecs) * 4;
+        const int r = row_of(i), d = (i - r * vecs) * 4;
         float mm, ll;
         const float4 v = both(r, d, mm, ll);
         __stcg(reinterpret_cast<float4*>(mine + gsize * 4 + r * p.head_dim + d), v);
@@ -1013,7 +1011,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       // Parts c, c + step, ... (`more` of them behind c) joined: f(row, column, result)
       auto join = [&](int c, int step, int more, auto&& f) {
         for (int i = tid; i < ng * vecs; i += kAttnThreads) {
-          const int r = i / vecs, d = (i % vecs) * 4;
+          const int r = row_of(i), d = (i - r * vecs) * 4;
           f(r, d, join_parts(part_of(c), part_of(c + more * step), more, 2 * step * static_cast<int64_t>(part_floats),
                              r * 4, gsize * 4 + r * p.head_dim + d));
         }
@@ -1032,12 +1030,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
             join(c, 1, more, [&](int r, int d, const Part& j) {
               __stcg(reinterpret_cast<float4*>(to + gsize * 4 + r * p.head_dim + d), j.v);
               if (d == 0) {
-                s_ml[0][r][0] = j.m;
-                s_ml[0][r][1] = j.l;
+                s_ml[0][r] = make_float2(j.m, j.l);
               }
             });
             __syncthreads();  // every thread has read the first part's (m, l)
-            if (tid < ng) __stcg(reinterpret_cast<float2*>(to + tid * 4), make_float2(s_ml[0][tid][0], s_ml[0][tid][1]));
+            if (tid < ng) __stcg(reinterpret_cast<float2*>(to + tid * 4), s_ml[0][tid]);
           }
         }
       }
@@ -1045,7 +1042,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       if (mine_last && comes_last(counters + wf, groups_of - 1))
         join(wf, step, groups_of - 1, [&](int r, int d, const Part& j) { write_row(r, d, j.v, j.m, j.l); });
     }
-    __syncthreads();  // the join buffers are free again
+    __syncthreads();  // the stages are free again
+    if (chunks < CPR) {
+      // the columns of the keys behind head_dim are zeros once more
+      for (int i = lane; i < KT * (CPR - chunks); i += 32)
+        *reinterpret_cast<uint4*>(smem + (w * ST + st) * S::STAGE +
+                                  staged<PITCH>(i / (CPR - chunks), chunks + i % (CPR - chunks))) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
   };
 
   int64_t item = i0 - at.t;  // first tile, among all T, of the item at `at`
@@ -1068,7 +1072,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         tile_mma(stage, mask);
     }
     if (at.t + 1 == at.nt || i + 1 == n) {
-      end_item(item, item + at.nt - 1);
+      end_item(item, item + at.nt - 1, stage);
       item += at.nt;
       at.next(p, units, CT);
       if (i + 1 < n) begin_item();
