@@ -215,7 +215,6 @@ constexpr int kMinTiles = 2;      // tiles a block takes at least
 constexpr int kFlatJoin = 24;     // parts of an item joined at once (see the kernel's end)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-
 // What a block does with a key/value head's query heads at a time:
 //   kFew   up to 4 (fp32: 1);  kSome  up to 8 (fp32: 4);  kMany  up to 16 (fp32: 8)
 enum Heads { kFew, kSome, kMany };
@@ -231,7 +230,8 @@ struct AttnShape {
   static constexpr int MAXG = F32 ? RG : HEADS == kFew ? 4 : RG;      // query heads of a block
   static constexpr int PITCH = DP * static_cast<int>(sizeof(C));      // bytes of a staged row
   static constexpr int KT0 = 4096 / PITCH;
-  static constexpr int KT = F32 ? 1024 / DP : KT0 > 32 || (E4M3 && NH == 2) ? 32 : KT0 < 16 ? 16 : KT0;  // keys of a warp's tile
+  // keys of a warp's tile: 8 KB a stage where the products allow it (16 to 32 keys)
+  static constexpr int KT = F32 ? 1024 / DP : KT0 > 32 || (E4M3 && NH == 2) ? 32 : KT0 < 16 ? 16 : KT0;
   static constexpr int CT = KT * kAttnWarps;
   static constexpr int STAGE = 2 * KT * PITCH;
   static constexpr int ST = STAGE <= 4096 ? 4 : 2;  // about 64 KB in a block's ring
@@ -245,7 +245,8 @@ struct AttnShape {
   static constexpr int REGS = F32 ? 128 : NH * (DP / 4 + (Q_SMEM ? 0 : DP / 8)) + 80;  // about what a thread needs
   static constexpr int BY_SMEM = 233472 / (SMEM + 1024 + 1024), BY_REGS = 65536 / (kAttnThreads * REGS);
   static constexpr int CTAS0 = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
-  static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > (NH == 2 && DP > 64 ? 2 : 3) ? (NH == 2 && DP > 64 ? 2 : 3) : CTAS0;  // blocks on an SM
+  static constexpr int MOST = NH == 2 && DP > 64 ? 2 : 3;
+  static constexpr int CTAS = CTAS0 < 1 ? 1 : CTAS0 > MOST ? MOST : CTAS0;  // blocks on an SM
 };
 
 // Chunk c of staged row `row`: 16-byte chunks are permuted within 128 bytes so
@@ -339,6 +340,9 @@ __device__ __forceinline__ RowInfo row_info(const AttnParams& p, int row, bool& 
   return r;
 }
 
+// Tiles of a row: one at least, so that a row without keys is written too.
+__device__ __forceinline__ int tiles_of(int len, int CT) { return len > 0 ? (len - 1) / CT + 1 : 1; }
+
 // A tile in a block's run: tile t of nt of row `row` and head unit h (a
 // key/value head and a group of its query heads).
 struct Cursor {
@@ -348,7 +352,7 @@ struct Cursor {
     const RowInfo r = row_info(p, row, bad);
     len = r.len;
     seq = r.seq;
-    nt = max(1, (len + CT - 1) / CT);
+    nt = tiles_of(len, CT);
   }
   __device__ __forceinline__ void next(const AttnParams& p, int units, int CT) {
     if (++t < nt) return;
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     int64_t sum = 0;
     bool bad = false;
 #pragma unroll 4
-    for (int r = r0; r < r1; ++r) sum += max(1, (row_info(p, r, bad).len + CT - 1) / CT);
+    for (int r = r0; r < r1; ++r) sum += tiles_of(row_info(p, r, bad).len, CT);
     if (bad && blockIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
     int64_t incl = sum;
 #pragma unroll
@@ -479,11 +483,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     int64_t at = (before + incl - sum) * units;  // first tile of this thread's rows
     if (i0 >= at && i0 < at + sum * units) {
       for (int r = r0; r < r1; ++r) {
-        const int nt = max(1, (row_info(p, r, bad).len + CT - 1) / CT);
+        const int nt = tiles_of(row_info(p, r, bad).len, CT);
         if (i0 < at + static_cast<int64_t>(nt) * units) {
           s_start[0] = r;
           s_start[1] = static_cast<int>(div_small(i0 - at, nt));
-          s_start[2] = static_cast<int>(i0 - at) - s_start[1] * nt;
+          s_start[2] = static_cast<int>(i0 - at - static_cast<int64_t>(s_start[1]) * nt);
           break;
         }
         at += static_cast<int64_t>(nt) * units;
