@@ -88,6 +88,8 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # _coda_marshal once the library is loaded
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class CodaError(RuntimeError):
@@ -114,8 +116,22 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             for name, (res, args) in SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
+            _load_marshal(lib)
             _lib = lib
     return _lib
+
+
+def _load_marshal(lib) -> None:
+    """The C marshalling of the short calls (coda_marshal.c), given the library's own entry points."""
+    global _fast
+    if _raw_stream is None or not os.path.exists(_build.MARSHAL):
+        return  # a PyTorch without CUDA: the checks in Python serve
+    from . import _coda_marshal as m
+    names = ("coda_paged_append", "coda_paged_attention", "coda_paged_attention_workspace_bytes", "coda_logprobs",
+             "coda_logprobs_backward")
+    m.init(torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.cuda.current_device,
+           _raw_stream, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    _fast = m
 
 
 def _check(status: int):
@@ -655,37 +671,30 @@ def coda_block_rowscale_fp8(A, amax_a, W1t, scale_w1, R, W2t, scale_w2, eps: flo
     return {"Aq": Aq, "scale_a": scale_a, "h": H, "P": P, "amax_h": amax_h, "Hq": Hq, "scale_h": scale_h, "Z": Z}
 
 
-# The decode and scoring calls are short on the GPU (a few microseconds), so their argument checks are made in one
-# pass that reads each tensor's properties once; only a call that it does not pass goes through _want and _dev, which
-# say what is wrong.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
+# The decode and scoring calls are short on the GPU (a few microseconds), so a good call is marshalled in C
+# (coda_marshal.c: the same checks, half the time); it hands back what it does not take, and the checks here say what
+# is wrong.
 
 def _pointers(specs):
     """Device pointers of (tensor or None, name, shape or None for one or more elements, dtype): contiguous CUDA tensors
-    on the current device, checked as by _want and _dev."""
-    try:
-        dev, out = torch.cuda.current_device() if specs[0][0].is_cuda else -2, []
-        for t, _, shape, dtype in specs:
-            if t is None:
-                out.append(None)
-            elif (t.dtype is dtype and (t.shape == shape if shape is not None else t.numel() > 0)
-                  and t.get_device() == dev and t.is_contiguous()):
-                out.append(t.data_ptr() or None)
-            else:
-                break
-        else:
-            return out
-    except AttributeError:
-        pass
+    on the current device, checked by _want and _dev."""
     for t, name, shape, dtype in specs:
-        _want(t, name, shape, None if dtype is None else (dtype,), numel=None if shape is not None else 1)
+        _want(t, name, shape, (dtype,), numel=None if shape is not None else 1)
     return [_dev(t, name) for t, name, _, _ in specs]
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    """_stream without building a stream object for the current one."""
-    return _raw_stream(t.get_device()) if stream is None and _raw_stream is not None else _stream(t, stream)
+def _stream_arg(stream):
+    """A stream argument for the C marshalling: None (the current one) or its address."""
+    return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _done(status):
+    """Whether the C marshalling made the call; raises if the library refused it."""
+    if status is None:
+        return False
+    if status:
+        _check(status)
+    return True
 
 
 def _cache_shape(k_cache, v_cache, dtype):
@@ -727,19 +736,22 @@ def coda_paged_append(Z, positions, page_table, k_cache, v_cache, q_heads: int, 
     already rotated.  Rows with a negative position are left out.  Returns the rotated queries [M, q_heads, head_dim],
     or None with ``want_q=False``."""
     lib = load_library()
+    if Q is None and want_q and k_cache.dim() == 4:
+        Q = torch.empty(Z.shape[0], q_heads, k_cache.shape[3], dtype=Z.dtype, device=Z.device)
+    if _fast is not None and _done(_fast.paged_append(Z, positions, row_seq, page_table, Q, k_cache, v_cache, scale_k,
+                                                      scale_v, q_heads, base, _stream_arg(stream))):
+        return Q
     M, dt = Z.shape[0], Z.dtype
     code = _dtype_code(Z)
     pages, kv_heads, page_size, D, ccode = _cache_shape(k_cache, v_cache, dt)
     seqs, max_pages = _table_shape(page_table)
-    if Q is None and want_q:
-        Q = torch.empty(M, q_heads, D, dtype=dt, device=Z.device)
     ptr = _pointers(((Z, "Z", (M, (q_heads + 2 * kv_heads) * D), dt), (positions, "positions", (M,), torch.int32),
                      (row_seq, "row_seq", (M,), torch.int32), (page_table, "page_table", page_table.shape, torch.int32),
                      (Q, "Q", (M, q_heads, D), dt), (k_cache, "k_cache", k_cache.shape, k_cache.dtype),
                      (v_cache, "v_cache", k_cache.shape, k_cache.dtype), (scale_k, "scale_k", None, torch.float32),
                      (scale_v, "scale_v", None, torch.float32)))
     _check(lib.coda_paged_append(*ptr[:7], M, seqs, max_pages, q_heads, kv_heads, D, pages, page_size, base, code, ccode,
-                                 ptr[7], ptr[8], _stream_of(Z, stream)))
+                                 ptr[7], ptr[8], _stream(Z, stream)))
     return Q
 
 
@@ -766,14 +778,18 @@ def coda_paged_attention(Q, k_cache, v_cache, page_table, lengths, workspace, *,
     if Q.dim() != 3:
         raise ValueError(f"Q has {Q.dim()} dimensions, expected [M, q_heads, head_dim]")
     M, q_heads, D = Q.shape
+    scale = D ** -0.5 if scale is None else scale
+    if O is None:
+        O = torch.empty(M, q_heads * D, dtype=Q.dtype, device=Q.device)
+    if _fast is not None and _done(_fast.paged_attention(Q, k_cache, v_cache, page_table, lengths, workspace, row_seq,
+                                                         scale, O, lse, scale_k, scale_v, _stream_arg(stream))):
+        return O
     dt, code = Q.dtype, _dtype_code(Q)
     pages, kv_heads, page_size, Dk, ccode = _cache_shape(k_cache, v_cache, dt)
     if Dk != D:
         raise ValueError(f"Q has head_dim {D}, the caches {Dk}")
     seqs, max_pages = _table_shape(page_table)
     _want(workspace, "workspace", nbytes=coda_paged_attention_workspace_bytes(q_heads, kv_heads, D))
-    if O is None:
-        O = torch.empty(M, q_heads * D, dtype=dt, device=Q.device)
     ptr = _pointers(((O, "O", (M, q_heads * D), dt), (k_cache, "k_cache", k_cache.shape, k_cache.dtype),
                      (v_cache, "v_cache", k_cache.shape, k_cache.dtype),
                      (page_table, "page_table", page_table.shape, torch.int32), (lengths, "lengths", (M,), torch.int32),
@@ -782,8 +798,8 @@ def coda_paged_attention(Q, k_cache, v_cache, page_table, lengths, workspace, *,
                      (workspace, "workspace", workspace.shape, workspace.dtype)))
     q_ptr, ldq = _rows(Q, "Q")
     _check(lib.coda_paged_attention(q_ptr, ldq, *ptr[1:6], ptr[0], ptr[6], M, seqs, max_pages, q_heads, kv_heads, D,
-                                    pages, page_size, D ** -0.5 if scale is None else scale, code, ccode, ptr[7],
-                                    ptr[8], ptr[9], _stream_of(Q, stream)))
+                                    pages, page_size, scale, code, ccode, ptr[7],
+                                    ptr[8], ptr[9], _stream(Q, stream)))
     return O
 
 
@@ -805,7 +821,6 @@ def coda_logprobs(logits, targets, top: int = 0, *, logp=None, entropy=None, lse
     if logits.dim() != 2:
         raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
     M, V = logits.shape
-    _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
     f32, e = torch.float32, lambda *shape, dt=torch.float32: torch.empty(*shape, dtype=dt, device=logits.device)
     out = {"logp": e(M) if logp is None else logp, "entropy": e(M) if entropy is None else entropy,
            "lse": e(M) if lse is None else lse}
@@ -814,11 +829,15 @@ def coda_logprobs(logits, targets, top: int = 0, *, logp=None, entropy=None, lse
         top_ids = out["top_ids"] = e(M, top, dt=torch.int32) if top_ids is None else top_ids
     else:
         top_logp = top_ids = None
+    if _fast is not None and _done(_fast.logprobs(logits, targets, top, out["logp"], out["entropy"], out["lse"],
+                                                  top_logp, top_ids, _stream_arg(stream))):
+        return out
+    _want(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
     ptr = _pointers(((targets, "targets", (M,), torch.int32), (out["logp"], "logp", (M,), f32),
                      (out["entropy"], "entropy", (M,), f32), (out["lse"], "lse", (M,), f32),
                      (top_logp, "top_logp", (M, top), f32), (top_ids, "top_ids", (M, top), torch.int32)))
     row, ld = _logits_rows(logits, "logits")
-    _check(lib.coda_logprobs(row, ld, *ptr, M, V, top, _dtype_code(logits), _stream_of(logits, stream)))
+    _check(lib.coda_logprobs(row, ld, *ptr, M, V, top, _dtype_code(logits), _stream(logits, stream)))
     return out
 
 
@@ -829,17 +848,20 @@ def coda_logprobs_backward(logits, targets, lse, entropy=None, dlogp=None, dentr
     if logits.dim() != 2:
         raise ValueError(f"logits has {logits.dim()} dimensions, expected [M, V]")
     M, V = logits.shape
-    f32 = torch.float32
-    _want(logits, "logits", dtypes=(f32, torch.bfloat16))
     if dlogits is None:  # rows on 16-byte boundaries, as the logits' own
         step = 16 // logits.element_size()
         dlogits = torch.empty(M, -(-V // step) * step, dtype=logits.dtype, device=logits.device)[:, :V]
+    if _fast is not None and _done(_fast.logprobs_backward(logits, targets, lse, entropy, dlogp, dentropy, dlogits,
+                                                           _stream_arg(stream))):
+        return dlogits
+    f32 = torch.float32
+    _want(logits, "logits", dtypes=(f32, torch.bfloat16))
     _want(dlogits, "dlogits", (M, V), (logits.dtype,))
     ptr = _pointers(((targets, "targets", (M,), torch.int32), (lse, "lse", (M,), f32), (entropy, "entropy", (M,), f32),
                      (dlogp, "dlogp", (M,), f32), (dentropy, "dentropy", (M,), f32)))
     row, ld = _logits_rows(logits, "logits")
     drow, ldd = _logits_rows(dlogits, "dlogits")
-    _check(lib.coda_logprobs_backward(row, ld, *ptr, drow, ldd, M, V, _dtype_code(logits), _stream_of(logits, stream)))
+    _check(lib.coda_logprobs_backward(row, ld, *ptr, drow, ldd, M, V, _dtype_code(logits), _stream(logits, stream)))
     return dlogits
 
 

@@ -2,6 +2,8 @@
 
 Each CUDA translation unit compiles in parallel to an object, then the objects
 link into one shared library exporting the C ABI of ``include/coda.h``.
+The argument marshalling of the short calls (coda_marshal.c) is a CPython
+extension module beside it, ``_coda_marshal.so``.
 Rebuilds only when a source, header or this script is newer than the library.
 """
 from __future__ import annotations
@@ -10,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcoda_gb300.so")
+MARSHAL = os.path.join(PKG, "_coda_marshal.so")
 
 SOURCES = ["coda_gemm_bf16.cu", "coda_gemm_tf32.cu", "coda_gemm_e4m3.cu", "coda_aux.cu", "coda_paged.cu",
            "coda_logprobs.cu", "coda_abi.cu"]
@@ -43,10 +47,23 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_marshal(cc: str) -> None:
+    """The extension module of coda_marshal.c, for the running Python."""
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(cc)), "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC") or "gcc", "-O2", "-fPIC", "-shared", "-std=gnu11", "-fvisibility=hidden", "-Wall",
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-isystem", cuda_include,
+           os.path.join(CSRC, "coda_marshal.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on coda_marshal.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -68,6 +85,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
+    build_marshal(cc)
     tmp = LIB + f".tmp{os.getpid()}"
     # The shared CUDA runtime: inside a PyTorch process the already-loaded
     # libcudart.so.13 is reused, so the library and torch agree on the
