@@ -213,6 +213,7 @@ constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxWorkers = 512;  // blocks of a grid: bounds the workspace
 constexpr int kMinTiles = 2;      // tiles a block takes at least
 constexpr int kFlatJoin = 24;     // parts of an item joined at once (see the kernel's end)
+constexpr int kJoinBatch = 16;    // parts fetched at a time
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What a block does with a key/value head's query heads at a time:
@@ -386,47 +387,11 @@ struct Runs {
   }
 };
 
-// The parts of a shared item joined in the order of the keys: the first, and
-// `more` others that lie `stride` floats apart, the last of them at `last`.
-// (m, l) is at `ml`, four columns of o at `v` of each.  8 parts are read at a
-// time (16 take registers from the loop over the keys): what this costs is a
-// trip to L2, about 1 us, for each batch.
+// Four columns of o of a part of an item, with its row's m and l.
 struct Part {
   float m, l;
   float4 v;
 };
-__device__ __forceinline__ Part join_parts(const float* first, const float* last, int more, int64_t stride, int ml, int v) {
-  constexpr int NB = 8;
-  Part a = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  for (int c0 = 0; c0 <= more; c0 += NB) {
-    float2 s[NB];
-    float4 x[NB];
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      s[u] = make_float2(-INFINITY, 0.0f);
-      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (c0 + u <= more) {
-        const float* part = c0 + u == 0 ? first : last - (more - c0 - u) * stride;
-        s[u] = __ldcg(reinterpret_cast<const float2*>(part + ml));
-        x[u] = __ldcg(reinterpret_cast<const float4*>(part + v));
-      }
-    }
-    float mn = a.m;
-#pragma unroll
-    for (int u = 0; u < NB; ++u) mn = fmaxf(mn, s[u].x);
-    const float base = mn == -INFINITY ? 0.0f : mn, k = ex2_approx(a.m - base);
-    a.m = mn;
-    a.l *= k;
-    a.v = make_float4(a.v.x * k, a.v.y * k, a.v.z * k, a.v.w * k);
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      const float f = ex2_approx(s[u].x - base);
-      a.l += s[u].y * f;
-      a.v = make_float4(a.v.x + x[u].x * f, a.v.y + x[u].y * f, a.v.z + x[u].z * f, a.v.w + x[u].w * f);
-    }
-  }
-  return a;
-}
 
 template <class E, class C, int DP, Heads HEADS>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS)
@@ -436,9 +401,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   constexpr bool F16 = S::E4M3;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kAttnWarps];
-  __shared__ int s_start[3], s_last;
+  __shared__ int s_start[5], s_last;
   __shared__ uint32_t s_mask[kAttnWarps][ST];
   __shared__ float2 s_ml[kAttnWarps][RG];  // (m, l) of the warps' parts of an item
+  __shared__ __align__(16) float2 s_joined[kJoinBatch][RG + (RG & 1)];  // (m, l) of the blocks' parts
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int G = p.q_heads / p.kv_heads, groups = (G + S::MAXG - 1) / S::MAXG, gsize = (G + groups - 1) / groups;
   const int units = p.kv_heads * groups;
@@ -459,8 +425,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     const int r0 = min(tid * per, p.M), r1 = min(r0 + per, p.M);
     int64_t sum = 0;
     bool bad = false;
+    RowInfo info = {0, 0};
 #pragma unroll 4
-    for (int r = r0; r < r1; ++r) sum += tiles_of(row_info(p, r, bad).len, CT);
+    for (int r = r0; r < r1; ++r) {
+      info = row_info(p, r, bad);
+      sum += tiles_of(info.len, CT);
+    }
     if (bad && blockIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
     int64_t incl = sum;
 #pragma unroll
@@ -483,9 +453,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     int64_t at = (before + incl - sum) * units;  // first tile of this thread's rows
     if (i0 >= at && i0 < at + sum * units) {
       for (int r = r0; r < r1; ++r) {
-        const int nt = tiles_of(row_info(p, r, bad).len, CT);
+        if (per > 1) info = row_info(p, r, bad);  // else it is still here
+        const int nt = tiles_of(info.len, CT);
         if (i0 < at + static_cast<int64_t>(nt) * units) {
           s_start[0] = r;
+          s_start[3] = info.len;
+          s_start[4] = info.seq;
           s_start[1] = static_cast<int>(div_small(i0 - at, nt));
           s_start[2] = static_cast<int>(i0 - at - static_cast<int64_t>(s_start[1]) * nt);
           break;
@@ -502,7 +475,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   in.row = s_start[0];
   in.h = s_start[1];
   in.t = s_start[2];
-  in.enter(p, CT);
+  in.len = s_start[3];
+  in.seq = s_start[4];
+  in.nt = tiles_of(in.len, CT);
   Cursor at = in;
   int pg, slot;
   bool bad_page = false;
@@ -915,9 +890,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     }
   };
 
-  // Counters [2][kMaxWorkers], then per block two parts of (m, l) [gsize] and o [gsize][head_dim]
+  // Counters [2][kMaxWorkers], then per block two parts of o [gsize][head_dim] and (m, l) [gsize], in 16-byte units
   unsigned* counters = static_cast<unsigned*>(p.workspace);
-  const int part_floats = gsize * (p.head_dim + 4);
+  const int part_floats = gsize * p.head_dim + ((gsize + 1) & ~1) * 2;
   float* parts = reinterpret_cast<float*>(counters + 2 * kMaxWorkers);
 
   auto write_row = [&](int r, int d, float4 v, float mm, float ll) {
@@ -999,8 +974,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         const int r = row_of(i), d = (i - r * vecs) * 4;
         float mm, ll;
         const float4 v = both(r, d, mm, ll);
-        __stcg(reinterpret_cast<float4*>(mine + gsize * 4 + r * p.head_dim + d), v);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(mine + r * 4), make_float2(mm, ll));
+        __stcg(reinterpret_cast<float4*>(mine + r * p.head_dim + d), v);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(mine + gsize * p.head_dim + r * 2), make_float2(mm, ll));
       }
       // The block that comes last of `others` + 1: its parts released (ordered before by the barrier), theirs acquired.
       auto comes_last = [&](unsigned* counter, int others) {
@@ -1012,12 +987,56 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         __syncthreads();
         return s_last != 0;
       };
-      // Parts c, c + step, ... (`more` of them behind c) joined: f(row, column, result)
+      // Parts c, c + step, ... (`more` of them behind c) joined in the order of the keys: f(row, column, result).  They
+      // are copied into the used stages, as many at a time as fit: what a batch costs is a trip to L2, about 1 us.
       auto join = [&](int c, int step, int more, auto&& f) {
-        for (int i = tid; i < ng * vecs; i += kAttnThreads) {
-          const int r = row_of(i), d = (i - r * vecs) * 4;
-          f(r, d, join_parts(part_of(c), part_of(c + more * step), more, 2 * step * static_cast<int64_t>(part_floats),
-                             r * 4, gsize * 4 + r * p.head_dim + d));
+        constexpr int VECS = (S::MAXG * DP / 4 + kAttnThreads - 1) / kAttnThreads;  // of a thread, at most
+        const int size = ng * vecs, fit = S::STAGE / (size * 16), batch = min(kJoinBatch, kAttnWarps * fit);
+        Part acc[VECS];
+#pragma unroll
+        for (int k = 0; k < VECS; ++k) acc[k] = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+        auto staged_part = [&](int u) { return smem + ((u % kAttnWarps) * ST + st) * S::STAGE + u / kAttnWarps * size * 16; };
+#pragma unroll 1
+        for (int c0 = 0; c0 <= more; c0 += batch) {
+          const int here = min(batch, more + 1 - c0);
+#pragma unroll 1
+          for (int u = 0; u < here; ++u) {
+            const float* part = part_of(c + (c0 + u) * step);
+            const uint32_t to = smem_u32(staged_part(u));
+            for (int i = tid; i < size; i += kAttnThreads) cp_async16(to + i * 16, part + i * 4, true);
+            if (tid < (ng + 1) / 2) cp_async16(smem_u32(&s_joined[u][2 * tid]), part + gsize * p.head_dim + tid * 4, true);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < VECS; ++k) {
+            const int i = tid + k * kAttnThreads;
+            if (i < size) {
+              const int r = row_of(i);
+              float mn = acc[k].m;
+#pragma unroll 4
+              for (int u = 0; u < here; ++u) mn = fmaxf(mn, s_joined[u][r].x);
+              const float base = mn == -INFINITY ? 0.0f : mn, old = ex2_approx(acc[k].m - base);
+              float l2 = acc[k].l * old;
+              float4 v = make_float4(acc[k].v.x * old, acc[k].v.y * old, acc[k].v.z * old, acc[k].v.w * old);
+#pragma unroll 4
+              for (int u = 0; u < here; ++u) {
+                const float2 ml = s_joined[u][r];
+                const float w1 = ex2_approx(ml.x - base);
+                const float4 x = *reinterpret_cast<const float4*>(staged_part(u) + i * 16);
+                l2 += ml.y * w1;
+                v = make_float4(v.x + x.x * w1, v.y + x.y * w1, v.z + x.z * w1, v.w + x.w * w1);
+              }
+              acc[k] = {mn, l2, v};
+            }
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < VECS; ++k) {
+          const int i = tid + k * kAttnThreads;
+          if (i < size) f(row_of(i), (i - row_of(i) * vecs) * 4, acc[k]);
         }
       };
       const int count = wl - wf + 1;
@@ -1032,13 +1051,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
           if (mine_last) {
             float* to = part_of(c);
             join(c, 1, more, [&](int r, int d, const Part& j) {
-              __stcg(reinterpret_cast<float4*>(to + gsize * 4 + r * p.head_dim + d), j.v);
+              __stcg(reinterpret_cast<float4*>(to + r * p.head_dim + d), j.v);
               if (d == 0) {
                 s_ml[0][r] = make_float2(j.m, j.l);
               }
             });
-            __syncthreads();  // every thread has read the first part's (m, l)
-            if (tid < ng) __stcg(reinterpret_cast<float2*>(to + tid * 4), s_ml[0][tid]);
+            __syncthreads();
+            if (tid < ng) __stcg(reinterpret_cast<float2*>(to + gsize * p.head_dim + tid * 2), s_ml[0][tid]);
           }
         }
       }
