@@ -404,7 +404,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   __shared__ int s_start[5], s_last;
   __shared__ uint32_t s_mask[kAttnWarps][ST];
   __shared__ float2 s_ml[kAttnWarps][RG];  // (m, l) of the warps' parts of an item
-  __shared__ __align__(16) float2 s_joined[kJoinBatch][RG + (RG & 1)];  // (m, l) of the blocks' parts
+  // the blocks' parts of an item as they are joined: (m, l), weight and weighted l, running m, next m and old weight
+  __shared__ float2 s_joined[kJoinBatch][RG], s_weight[kJoinBatch][RG], s_next[RG];
+  __shared__ float s_run[RG];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int G = p.q_heads / p.kv_heads, groups = (G + S::MAXG - 1) / S::MAXG, gsize = (G + groups - 1) / groups;
   const int units = p.kv_heads * groups;
@@ -994,41 +996,62 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         const int size = ng * vecs, fit = S::STAGE / (size * 16), batch = min(kJoinBatch, kAttnWarps * fit);
         Part acc[VECS];
 #pragma unroll
-        for (int k = 0; k < VECS; ++k) acc[k] = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-        auto staged_part = [&](int u) { return smem + ((u % kAttnWarps) * ST + st) * S::STAGE + u / kAttnWarps * size * 16; };
+        for (int k = 0; k < VECS; ++k) acc[k] = {0.0f, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+        if (tid < RG) s_run[tid] = -INFINITY;
+        // part u of a batch lies in the stage of warp u mod 4, behind u / 4 others
+        const uint32_t to = smem_u32(smem) + st * S::STAGE + tid * 16;
+        const uint8_t* from = smem + st * S::STAGE + tid * 16;
 #pragma unroll 1
         for (int c0 = 0; c0 <= more; c0 += batch) {
           const int here = min(batch, more + 1 - c0);
-#pragma unroll 1
+#pragma unroll 4
           for (int u = 0; u < here; ++u) {
-            const float* part = part_of(c + (c0 + u) * step);
-            const uint32_t to = smem_u32(staged_part(u));
-            for (int i = tid; i < size; i += kAttnThreads) cp_async16(to + i * 16, part + i * 4, true);
-            if (tid < (ng + 1) / 2) cp_async16(smem_u32(&s_joined[u][2 * tid]), part + gsize * p.head_dim + tid * 4, true);
+            const float* part = part_of(c + (c0 + u) * step) + tid * 4;
+            const uint32_t at_u = to + (u & 3) * ST * S::STAGE + (u >> 2) * size * 16;
+#pragma unroll
+            for (int k = 0; k < VECS; ++k)
+              if (tid + k * kAttnThreads < size)
+                cp_async16(at_u + k * kAttnThreads * 16, part + k * kAttnThreads * 4, true);
           }
           cp_async_commit();
+          for (int x = tid; x < here * ng; x += kAttnThreads) {
+            const int u = x / ng, r = x - u * ng;
+            s_joined[u][r] = __ldcg(reinterpret_cast<const float2*>(part_of(c + (c0 + u) * step) + gsize * p.head_dim + r * 2));
+          }
           cp_async_wait<0>();
           __syncthreads();
+          // the parts' weights, once for each part and row
+          for (int x = tid; x < here * ng; x += kAttnThreads) {
+            const int u = x / ng, r = x - u * ng;
+            const float old = s_run[r];
+            float mn = old;
+#pragma unroll 4
+            for (int y = 0; y < here; ++y) mn = fmaxf(mn, s_joined[y][r].x);
+            const float base = mn == -INFINITY ? 0.0f : mn, w1 = ex2_approx(s_joined[u][r].x - base);
+            s_weight[u][r] = make_float2(w1, s_joined[u][r].y * w1);
+            if (u == 0) s_next[r] = make_float2(mn, ex2_approx(old - base));
+          }
+          __syncthreads();
+          if (tid < ng) s_run[tid] = s_next[tid].x;
 #pragma unroll
           for (int k = 0; k < VECS; ++k) {
             const int i = tid + k * kAttnThreads;
             if (i < size) {
               const int r = row_of(i);
-              float mn = acc[k].m;
-#pragma unroll 4
-              for (int u = 0; u < here; ++u) mn = fmaxf(mn, s_joined[u][r].x);
-              const float base = mn == -INFINITY ? 0.0f : mn, old = ex2_approx(acc[k].m - base);
+              const float old = s_next[r].y;
+              acc[k].m = s_next[r].x;
               float l2 = acc[k].l * old;
               float4 v = make_float4(acc[k].v.x * old, acc[k].v.y * old, acc[k].v.z * old, acc[k].v.w * old);
 #pragma unroll 4
               for (int u = 0; u < here; ++u) {
-                const float2 ml = s_joined[u][r];
-                const float w1 = ex2_approx(ml.x - base);
-                const float4 x = *reinterpret_cast<const float4*>(staged_part(u) + i * 16);
-                l2 += ml.y * w1;
-                v = make_float4(v.x + x.x * w1, v.y + x.y * w1, v.z + x.z * w1, v.w + x.w * w1);
+                const float2 wl = s_weight[u][r];
+                const float4 x = *reinterpret_cast<const float4*>(from + (u & 3) * ST * S::STAGE + (u >> 2) * size * 16 +
+                                                                  k * kAttnThreads * 16);
+                l2 += wl.y;
+                v = make_float4(v.x + x.x * wl.x, v.y + x.y * wl.x, v.z + x.z * wl.x, v.w + x.w * wl.x);
               }
-              acc[k] = {mn, l2, v};
+              acc[k].l = l2;
+              acc[k].v = v;
             }
           }
           __syncthreads();
