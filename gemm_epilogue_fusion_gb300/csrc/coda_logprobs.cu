@@ -131,7 +131,7 @@ struct Sums {
   }
 };
 
-constexpr int kRowThreads = 512, kRowVecs = 4;  // threads of a block, vectors of a thread in flight
+constexpr int kRowVecs = 4;  // vectors of a thread in flight
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 
@@ -554,26 +554,40 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const _
   }
 }
 
-// One block per row: NT threads; few rows: clusters of blocks of 512 threads.
-template <class E, int NT>
-cudaError_t run_logprobs(LogprobsParams p, int64_t M, cudaStream_t s, bool pdl) {
-  // up to 8 blocks share a row, as long as the rows leave SMs idle and each block has at least one round of loads
-  constexpr int VEC = 16 / sizeof(E), WIDE = 512;
-  int c = 1;
-  while (c < kMaxCluster && M * c * 2 <= device_sm_count() && p.V / (c * 2) >= WIDE * VEC) c *= 2;
+template <class E, int NT, bool CLUSTER>
+cudaError_t run_logprobs(LogprobsParams p, int64_t M, int c, cudaStream_t s, bool pdl) {
   p.ranks = c;
   void* args[] = {&p};
-  const void* k = c > 1 ? reinterpret_cast<const void*>(logprobs_kernel<E, WIDE, true>)
-                        : reinterpret_cast<const void*>(logprobs_kernel<E, NT, false>);
-  return launch_ex(k, dim3(static_cast<unsigned>(M * c)), dim3(c > 1 ? WIDE : NT), 0, s, pdl, args, c);
+  return launch_ex(reinterpret_cast<const void*>(logprobs_kernel<E, NT, CLUSTER>), dim3(static_cast<unsigned>(M * c)),
+                   dim3(NT), 0, s, pdl, args, c);
+}
+
+// How many threads take a row (us for M rows of V bf16 logits, 8 alternatives, by 128 / 256 / 512 threads):
+//   many rows   4096 x 8192: 25 / 29 / 51    4096 x 16000: 36 / 40 / 52    4096 x 32000: 57 / 57 / 68
+//               4096 x 50264: 92 / 81 / 94   2048 x 65536: 66 / 54 / 55    2048 x 128256: 134 / 104 / 92
+//   few rows    64 x 16000: 7.0 / 5.2 / 4.3  200 x 16000: 7.6 / 6.0 / 5.7  400 x 50264: 15.4 / 12.1 / 11.9
+// so few rows (one wave of the largest blocks) take 512 threads, many rows fewer while they are short: the serial end
+// of a row costs more blocks less.
+// One row or a few that are long take a cluster: 1 x 128256 in 9.0 / 8.3 / 6.9 / 6.9 us by 1 / 2 / 4 / 8 blocks of 512,
+// 1 x 200000 in 13.0 / 10.0 / 8.1 / 7.1, but 1 x 50264 in 6.1 / 7.0 / 6.9 / 7.0 and 76 x 128256 in 9.4 by one and 8.7 by
+// two.  From 4.5 rounds of loads a row is split until a block has one round, or the blocks fill the SMs.
+template <class E>
+cudaError_t pick_logprobs(const LogprobsParams& p, int64_t M, cudaStream_t s, bool pdl) {
+  constexpr int64_t ROUND = 512 * kRowVecs * (16 / sizeof(E));
+  const int sms = device_sm_count();
+  int c = 1;
+  if (p.V * 2 >= ROUND * 9)
+    while (c < kMaxCluster && M * c * 2 <= sms && p.V > ROUND * c) c *= 2;
+  if (c > 1) return run_logprobs<E, 512, true>(p, M, c, s, pdl);
+  const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(E);
+  if (M <= 3 * sms || bytes > 128 * 1024) return run_logprobs<E, 512, false>(p, M, 1, s, pdl);
+  return bytes > 48 * 1024 ? run_logprobs<E, 256, false>(p, M, 1, s, pdl) : run_logprobs<E, 128, false>(p, M, 1, s, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobsParams& p, int64_t M, bool f32, cudaStream_t s, bool pdl) {
-  // short rows take small blocks
-  if (p.V <= 8192) return f32 ? run_logprobs<float, 128>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, 128>(p, M, s, pdl);
-  return f32 ? run_logprobs<float, kRowThreads>(p, M, s, pdl) : run_logprobs<__nv_bfloat16, kRowThreads>(p, M, s, pdl);
+  return f32 ? pick_logprobs<float>(p, M, s, pdl) : pick_logprobs<__nv_bfloat16>(p, M, s, pdl);
 }
 
 int64_t logprobs_backward_blocks(int64_t V, bool f32) {

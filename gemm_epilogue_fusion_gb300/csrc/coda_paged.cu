@@ -235,7 +235,7 @@ struct AttnShape {
   static constexpr int KT = F32 ? 1024 / DP : KT0 > 32 || (E4M3 && NH == 2) ? 32 : KT0 < 16 ? 16 : KT0;
   static constexpr int CT = KT * kAttnWarps;
   static constexpr int STAGE = 2 * KT * PITCH;
-  static constexpr int ST = STAGE <= 4096 ? 4 : 2;  // about 64 KB in a block's ring
+  static constexpr int ST = 2;  // stages of a ring: one more tile in flight made 162 us 169 (64 ragged rows)
   static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
   static constexpr int RING = kAttnWarps * ST * STAGE;
   // the widest shape keeps its queries in shared memory: 64 registers a thread that o needs

@@ -50,7 +50,8 @@ def check_forward(x, targets, top):
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M,V,top", [(1, 1, 1), (1, 1, 0), (3, 2, 2), (2, 7, 5), (5, 64, 64), (4, 100, 20), (1, 257, 3),
                                      (7, 1000, 1), (3, 4096, 50), (2, 8193, 64), (300, 515, 8), (1, 50257, 20),
-                                     (5, 32000, 0), (160, 9999, 5), (1, 200001, 64), (20, 33001, 12)])
+                                     (5, 32000, 0), (160, 9999, 5), (1, 200001, 64), (20, 33001, 12),
+                                     (1, 73729, 20), (40, 90001, 12), (500, 9999, 5), (460, 25001, 3), (1500, 603, 8)])
 def test_logprobs_against_64_bits(dt, M, V, top):
     g = U.gen(M * 7 + V)
     x = (torch.randn(M, V, generator=g) * 3).to(dt)
@@ -60,7 +61,8 @@ def test_logprobs_against_64_bits(dt, M, V, top):
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("kind", ["equal", "rising", "falling", "few values", "blocks", "one large"])
-@pytest.mark.parametrize("M,V", [(2, 40000), (170, 6001), (100, 12001)])
+@pytest.mark.parametrize("M,V", [(2, 40000), (170, 6001), (100, 12001), (3, 100001), (500, 3001),
+                                 (470, 13001)])
 def test_alternatives_in_hard_orders(dt, kind, M, V):
     """Ties by the lower index, and orders in which every element beats those before it."""
     g = U.gen(V)
@@ -75,7 +77,7 @@ def test_alternatives_in_hard_orders(dt, kind, M, V):
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("V", [20, 5000, 70000])
+@pytest.mark.parametrize("V", [20, 5000, 70000, 150001])
 def test_masked_logits(dt, V):
     """Rows with -inf, with the type's lowest value, with nothing left, and with one value left."""
     low = torch.finfo(dt).min
@@ -207,7 +209,7 @@ def test_gradient_against_differences():
         assert abs((grad * u).sum() - want) <= 1e-5 * (1 + (grad * u).abs().sum())
 
 
-@pytest.mark.parametrize("M,V", [(30, 5001), (1, 50257), (100, 20000)])
+@pytest.mark.parametrize("M,V", [(30, 5001), (1, 50257), (100, 20000), (2, 128256), (500, 5001)])
 def test_logprobs_on_another_stream_and_in_a_graph(M, V):
     """Captured and replayed on other values in the same buffer, the bits are the eager calls'."""
     import gemm_epilogue_fusion_gb300 as gg
@@ -258,10 +260,10 @@ def test_rows_behind_2_to_the_31_elements():
     assert abs(float(g2[-1, 77]) - (1 - p)) <= 2.0 ** -8 * (1 - p) + 1e-6 and (g2[-2] == 0).all()
 
 
-@pytest.mark.parametrize("M", [1, 7, 100, 700])
-def test_the_same_bits_on_every_call(M):
+@pytest.mark.parametrize("M,V", [(1, 20011), (7, 20011), (100, 20011), (700, 20011), (700, 30011), (5, 100003)])
+def test_the_same_bits_on_every_call(M, V):
     import gemm_epilogue_fusion_gb300 as gg
-    x = (torch.randn(M, 20011, generator=U.gen(M)) * 3).to(BF)
+    x = (torch.randn(M, V, generator=U.gen(M)) * 3).to(BF)
     x[:, 5000:9000] = x[:, 4999:5000]  # thousands of ties
     xd, t = padded(x), torch.full((M,), 17, dtype=torch.int32).cuda()
     first = {k: v.clone() for k, v in gg.coda_logprobs(xd, t, 30).items()}
