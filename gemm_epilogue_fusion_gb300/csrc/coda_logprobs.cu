@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
   Sums a = {m, s2.x + s2.y, t2.x + t2.y};
   if (!(m < INFINITY)) {
     a.s = a.t = NAN;  // +inf or NaN
-  } else if (fabsf(m) > kHuge) {
+  } else if (fabsf(m) >= kHuge) {
     a.s = a.t = 0.0f;  // no weight beside an ordinary logit (and see `careful`)
   } else {
     const float off = fmaf(m, kLog2e, -base), c = ex2_approx(-off);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
     }
   }
   __syncthreads();
-  if (__builtin_expect(fabsf(sh.part.m) > kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
+  if (__builtin_expect(fabsf(sh.part.m) >= kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
     // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
     const float top = sh.part.m;
     a = {top, 0.0f, 0.0f};

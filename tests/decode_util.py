@@ -116,7 +116,7 @@ def logprobs(x, targets, top):
 
 def logprobs_bounds(x, ref):
     """Bounds of lse (and every log probability), and of the entropy.  A thread adds at most V/256 + 64 terms one by
-    one (256 threads or more a row), the exponentials are off by 2^-21, x - lse rounds twice at the size of its parts;
+    one (128 threads or more a row, two sums each), the exponentials are off by 2^-21, x - lse rounds twice at the size of its parts;
     the entropy's terms carry |x - max| as well."""
     V = x.shape[1]
     rel = (V / 256 + 64) * 2.0 ** -24 + 2.0 ** -20

@@ -114,6 +114,30 @@ def test_masked_logits(dt, V):
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,V", [(5, 300), (500, 300), (5, 40001), (5, 90001)])
+def test_logits_at_the_limit_of_the_packed_arithmetic(dt, M, V):
+    """Rows whose largest logit is -2^126 or 2^126, beside -inf, equal and ordinary ones."""
+    x = torch.full((M, V), -math.inf)
+    x[0, 7] = -2.0 ** 126
+    x[1] = -2.0 ** 126
+    x[2, 3:9] = 2.0 ** 126
+    x[3, ::3] = torch.randn(x[3, ::3].shape, generator=U.gen(V))
+    x[3, 1] = -2.0 ** 126
+    x[4:] = 0.0
+    import gemm_epilogue_fusion_gb300 as gg
+    t = torch.full((M,), 7, dtype=torch.int32)
+    t[3] = 3
+    got = {k: v.cpu() for k, v in gg.coda_logprobs(padded(x.to(dt)), t.cuda(), 6).items()}
+    ref = U.logprobs(x.to(dt), t, 6)
+    lp = [0.0, -math.log(V), -math.log(6), float(ref["logp"][3])] + [-math.log(V)] * (M - 4)
+    ent = [0.0, math.log(V), math.log(6), float(ref["entropy"][3])] + [math.log(V)] * (M - 4)
+    # log V plus the sums' 2^-20, and x - lse's rounding at the size of row 3
+    for k, want in (("logp", lp), ("entropy", ent)):
+        assert ((got[k].to(U.F64) - torch.tensor(want, dtype=U.F64)).abs() <= 2.0 ** -16).all(), k
+    assert torch.equal(got["top_ids"], ref["top_ids"])
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 def test_nan_infinite_and_unscored(dt):
     import gemm_epilogue_fusion_gb300 as gg
     V = 3001
