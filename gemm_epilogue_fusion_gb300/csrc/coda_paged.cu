@@ -547,6 +547,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   constexpr int KS = DP / 16;
   // kFew, bf16: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to bf16;
   // kSome, bf16: a second product does.  f16 weights (e4m3 caches) lose 2^-11, kMany rounds once (2^-8 at most).
+  // f16 weights are taken 2^15 times as large: 2^-29 of the largest is still a normal number, and what vanishes below
+  // 2^-40 of it is no 2^-20 of a row's sum in 10^6 keys.
+  constexpr float UP = F16 ? 15.0f : 0.0f;
   constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && !F16 && HEADS == kSome;
   float o[OW], m[NR], l[NR];
   uint32_t q[S::F32 ? 1 : NH * KS * 2] = {};
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float base = m[r] == -INFINITY ? 0.0f : m[r];
+      const float base = m[r] == -INFINITY ? 0.0f : m[r] - UP;
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       uint2 u = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
       *reinterpret_cast<uint2*>(dst) = u;
     }
-    if (p.lse && d == 0) p.lse[head] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    if (p.lse && d == 0) p.lse[head] = ll == 0.0f ? -INFINITY : (mm - UP + log2f(ll)) * kLn2;
   };
 
   // The warps' parts of the item at `at` joined, and written out or left for the last block.  first_tile, last_tile: of

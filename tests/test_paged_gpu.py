@@ -275,6 +275,28 @@ def test_attention_splits_the_length(types, lens):
 
 
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
+@pytest.mark.parametrize("hq", [8, 24, 48])
+def test_attention_keeps_the_small_weights_beside_a_large_one(types, hq):
+    """One key with 2^25 times the others' weight and no value: the output is what the others add up to."""
+    import gemm_epilogue_fusion_gb300 as gg
+    M, hkv, d, page, n = 24, 4, 16, 64, 16384
+    q, k, v, table, _, s = make(1, hkv, d, page, [n], types, hq, poison=False)
+    q = torch.ones(M, hq, d).to(types[0])
+    k.view(torch.uint8).zero_()
+    at = int(table[0, 0])
+    k.view(torch.uint8 if types[1] == E4 else types[1])[at, :, 5] = (
+        torch.tensor(208.0).to(E4).view(torch.uint8) if types[1] == E4 else 4.5)
+    v = (v.float().abs() + 8).to(types[1])
+    v.view(torch.uint8 if types[1] == E4 else types[1])[at, :, 5] = 0
+    row_seq, ln = torch.zeros(M, dtype=torch.int32), torch.full((M,), n, dtype=torch.int32)
+    ws = gg.paged_attention_workspace(hq, hkv, d, "cuda")
+    lse = torch.empty(M, hq).cuda()
+    o = gg.coda_paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ln.cuda(), ws, lse=lse,
+                                row_seq=row_seq.cuda(), **scales(types[1], s))
+    check(q, k, v, table, ln, s, o, lse, row_seq=row_seq.tolist())
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
 def test_attention_rows_of_one_sequence_strided_queries_and_scale(types):
     """Several new tokens of one sequence, each with its own length; queries read out of a QKV product's rows."""
     import gemm_epilogue_fusion_gb300 as gg
