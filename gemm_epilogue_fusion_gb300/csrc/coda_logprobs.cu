@@ -131,18 +131,18 @@ struct Sums {
   }
 };
 
-constexpr int kRowVecs = 4;  // vectors of a thread in flight
+constexpr int kRowVecs = 4;  // vectors of a thread in flight (figures below)
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 
 template <int NT>
 struct LogprobsShared {
   Sums warp[NT / 32];
-  uint32_t tops[128];     // each warp's largest thread maxima
+  __align__(16) uint32_t tops[128];  // each warp's largest thread maxima
   uint32_t bound;
   int owner[NT];          // threads whose largest value reaches the bound
   int owners, found;
-  uint64_t cand[kCandidates];
+  __align__(16) uint64_t cand[kCandidates];
   uint64_t red[NT / 32];
   // what the cluster's first block collects
   Sums part;
@@ -158,13 +158,18 @@ struct LogprobsShared {
 // largest value reaches it can hold an alternative, each with 1 / NT of the
 // row, so their elements are read once more, from L2 as a rule: 20 of 512
 // threads are 4% of the row.  The few elements that reach the bound are ranked
-// by counting.  If ties leave more than kCandidates of them, the alternatives
-// are found one by one instead.
+// by counting.  If ties leave more than kCandidates of them (512 to 2048 make
+// no difference otherwise), the alternatives are found one by one instead.
 //
 // Bound by the row's bytes.  bf16 costs about 5 issue slots an element (the
-// arithmetic is packed in pairs) of the 11 that the HBM rate leaves.
+// arithmetic is packed in pairs) of the 11 that the HBM rate leaves.  2048 rows
+// of 128256 bf16 logits take 82 us without alternatives (6.4 TB/s), 92 with 8
+// (5.7 TB/s), 99 with 20 and 124 with 64: the end of a row costs its block
+// about as long as 1 / 8 of the row.  kRowVecs of 2 / 3 / 4 / 6 made that
+// 102 / 98 / 92 / 103; a ring of cp.async stages that ran across the rows 130;
+// the bound found by bits over all warps 106.
 template <class E, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+__global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   constexpr int VEC = 16 / sizeof(E), U = kRowVecs;
   __shared__ LogprobsShared<NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -253,25 +258,43 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
   // ---- the bound of the alternatives: each warp's `each` largest keys (taken out one by one), of all of those the
   // top-th.  top threads reach it, and with one or two more a warp than top needs few others do.
   if (p.top > 0) {
-    const int each = (p.top + NT / 32 - 1) / (NT / 32) + 1, n = each * (NT / 32);
-    uint32_t k = key;
-    for (int e = 0; e < each; ++e) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, k);
-      if (lane == 0) sh.tops[e * (NT / 32) + w] = best;
-      if (lane == __ffs(__ballot_sync(0xffffffffu, k == best)) - 1) k = 0;
-    }
-    __syncthreads();
-    // ranks by counting, a warp for each key; the lower place counts as larger among equals
+    const int warps = max(min(NT / 32, (v1 - v0 + 31) / 32), 1);  // that have elements
+    const int each = min(warps == NT / 32 ? (p.top + NT / 32 - 1) / (NT / 32) + 1 : (p.top + warps - 1) / warps + 1, 32);
+    const int n = warps * each, n4 = (n + 3) & ~3;
+    if (w < warps) {
+      uint32_t k = key;
 #pragma unroll 1
-    for (int c = w; c < n; c += NT / 32) {
-      const uint32_t mine = sh.tops[c];
-      int before = 0;
-#pragma unroll 1
-      for (int o = lane; o < ((n + 31) & ~31); o += 32) {
-        const uint32_t other = o < n ? sh.tops[o] : 0u;
-        before += __popc(__ballot_sync(0xffffffffu, o < n && (other > mine || (other == mine && o < c))));
+      for (int e = 0; e < each; ++e) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, k);
+        if (lane == 0) sh.tops[e * warps + w] = best;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, k == best)) - 1) k = 0;
       }
-      if (before == p.top - 1) sh.bound = mine;  // one key has this rank
+    }
+    if (tid < n4 - n) sh.tops[n + tid] = 0;
+    if (tid == 0) sh.bound = 0;
+    __syncthreads();
+    // how many are above a key, and how many reach it: up to 32 keys lie in a warp's lanes, else a thread counts for each
+    if (n <= 32) {
+      const uint32_t all = lane < n4 ? sh.tops[lane] : 0u;
+#pragma unroll 1
+      for (int c = w; c < n; c += NT / 32) {
+        const uint32_t mine = __shfl_sync(0xffffffffu, all, c);
+        const int above = __popc(__ballot_sync(0xffffffffu, all > mine)), reach = __popc(__ballot_sync(0xffffffffu, all >= mine));
+        if (above < p.top && reach >= p.top) sh.bound = mine;  // the same value from all that write it
+      }
+    } else {
+#pragma unroll 1
+      for (int c = tid; c < n; c += NT) {
+        const uint32_t mine = sh.tops[c];
+        int above = 0, reach = 0;
+#pragma unroll 2
+        for (int o = 0; o < n4; o += 4) {
+          const uint4 t = *reinterpret_cast<const uint4*>(sh.tops + o);
+          above += (t.x > mine) + (t.y > mine) + (t.z > mine) + (t.w > mine);
+          reach += (t.x >= mine) + (t.y >= mine) + (t.z >= mine) + (t.w >= mine);
+        }
+        if (above < p.top && reach >= p.top) sh.bound = mine;
+      }
     }
     __syncthreads();
   }
@@ -300,17 +323,26 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
         for (int u = 0; u < U; ++u) collect(q[u], v0 + tid + u * NT < v1 ? v0 + tid + u * NT : vecs);
       }
     } else {
-      if (owner) sh.owner[atomicAdd(&sh.owners, 1)] = tid;
+      const uint32_t mask = __ballot_sync(0xffffffffu, owner);
+      int at = 0;
+      if (lane == 0 && mask != 0) at = atomicAdd(&sh.owners, __popc(mask));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
+      if (owner) sh.owner[at] = tid;
       __syncthreads();
-      const int owners = sh.owners, u0 = w < owners ? v0 + sh.owner[w] + lane * NT : v1;
+      // the owners' vectors dealt to the threads, 2^shift an owner (a few more than it has)
+      const int mine = (v1 - v0 + NT - 1) / NT, shift = mine > 1 ? 32 - __clz(mine - 1) : 0, all = sh.owners << shift;
+      auto place = [&](int k) { return k < all ? v0 + sh.owner[k >> shift] + (k & ((1 << shift) - 1)) * NT : v1; };
+      int u = place(tid);
       uint4 vec;
-      if (u0 < v1) vec = load_vec<E>(x, u0, p.V);
-      warp_sums();  // while the first owner's elements are on their way
+      if (u < v1) vec = load_vec<E>(x, u, p.V);
+      warp_sums();  // while the elements are on their way
       sums_done = true;
-      if (u0 < v1) collect(vec, u0);
-      for (int u = u0 + 32 * NT; u < v1; u += 32 * NT) collect(load_vec<E>(x, u, p.V), u);
-      for (int o = w + NT / 32; o < owners; o += NT / 32)
-        for (int u = v0 + sh.owner[o] + lane * NT; u < v1; u += 32 * NT) collect(load_vec<E>(x, u, p.V), u);
+#pragma unroll 1
+      for (int k = tid; k < all; k += NT) {
+        if (u < v1) collect(vec, u);
+        u = place(k + NT);
+        if (u < v1) vec = load_vec<E>(x, u, p.V);
+      }
     }
   }
   if (!sums_done) warp_sums();
@@ -324,14 +356,26 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 1 : 1536 / NT) logprobs_kernel(c
   if (p.top > 0) {
     const int n = sh.found;
     if (__builtin_expect(n <= kCandidates, 1)) {
+      if (n <= 32) {
+        const uint64_t all = lane < n ? sh.cand[lane] : 0u;
 #pragma unroll 1
-      for (int c = w; c < n; c += NT / 32) {
-        const uint64_t mine = sh.cand[c];
-        int before = 0;
+        for (int c = w; c < n; c += NT / 32) {
+          const uint64_t mine = sh.cand[c];
+          const int before = __popc(__ballot_sync(0xffffffffu, all > mine));
+          if (before < local) sh.best[before] = mine;
+        }
+      } else {
 #pragma unroll 1
-        for (int o = lane; o < ((n + 31) & ~31); o += 32)
-          before += __popc(__ballot_sync(0xffffffffu, o < n && sh.cand[o] > mine));
-        if (before < local) sh.best[before] = mine;
+        for (int c = tid; c < n; c += NT) {  // a thread for each counts those above it
+          const uint64_t mine = sh.cand[c];
+          int before = n & 1 ? sh.cand[n - 1] > mine : 0;
+#pragma unroll 2
+          for (int o = 0; o + 1 < n; o += 2) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(sh.cand + o);
+            before += (t.x > mine) + (t.y > mine);
+          }
+          if (before < local) sh.best[before] = mine;
+        }
       }
     } else {
       uint64_t below = ~0ull;
@@ -562,12 +606,12 @@ cudaError_t run_logprobs(LogprobsParams p, int64_t M, int c, cudaStream_t s, boo
                    dim3(NT), 0, s, pdl, args, c);
 }
 
-// How many threads take a row (us for M rows of V bf16 logits, 8 alternatives, by 128 / 256 / 512 threads):
-//   many rows   4096 x 8192: 25 / 29 / 51    4096 x 16000: 36 / 40 / 52    4096 x 32000: 57 / 57 / 68
-//               4096 x 50264: 92 / 81 / 94   2048 x 65536: 66 / 54 / 55    2048 x 128256: 134 / 104 / 92
-//   few rows    64 x 16000: 7.0 / 5.2 / 4.3  200 x 16000: 7.6 / 6.0 / 5.7  400 x 50264: 15.4 / 12.1 / 11.9
-// so few rows (one wave of the largest blocks) take 512 threads, many rows fewer while they are short: the serial end
-// of a row costs more blocks less.
+// How many threads take a row (us for M rows of V bf16 logits with 8 alternatives, by 128 / 256 / 512 threads):
+//   many rows   4096 x 1000: 17 / 24 / 41    4096 x 16000: 32 / 36 / 51   4096 x 32000: 56 / 53 / 68
+//               4096 x 50264: 89 / 80 / 93   2048 x 65536: 63 / 53 / 54   2048 x 128256: 131 / 100 / 92
+//   few rows    64 x 16000: 6.0 / 4.7 / 4.7  200 x 16000: 6.4 / 5.3 / 5.9  400 x 8192: 5.3 / 5.4 / 7.9
+// so rows that leave SMs idle take 512 threads, many rows fewer while they are short: a row's serial end, which finds
+// its alternatives, then leaves more of the SM to other rows.
 // One row or a few that are long take a cluster: 1 x 128256 in 9.0 / 8.3 / 6.9 / 6.9 us by 1 / 2 / 4 / 8 blocks of 512,
 // 1 x 200000 in 13.0 / 10.0 / 8.1 / 7.1, but 1 x 50264 in 6.1 / 7.0 / 6.9 / 7.0 and 76 x 128256 in 9.4 by one and 8.7 by
 // two.  From 4.5 rounds of loads a row is split until a block has one round, or the blocks fill the SMs.
@@ -580,7 +624,7 @@ cudaError_t pick_logprobs(const LogprobsParams& p, int64_t M, cudaStream_t s, bo
     while (c < kMaxCluster && M * c * 2 <= sms && p.V > ROUND * c) c *= 2;
   if (c > 1) return run_logprobs<E, 512, true>(p, M, c, s, pdl);
   const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(E);
-  if (M <= 3 * sms || bytes > 128 * 1024) return run_logprobs<E, 512, false>(p, M, 1, s, pdl);
+  if (M <= 2 * sms || bytes > 128 * 1024) return run_logprobs<E, 512, false>(p, M, 1, s, pdl);
   return bytes > 48 * 1024 ? run_logprobs<E, 256, false>(p, M, 1, s, pdl) : run_logprobs<E, 128, false>(p, M, 1, s, pdl);
 }
 
