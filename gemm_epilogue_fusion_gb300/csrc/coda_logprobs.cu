@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
 
 // Gradient: element by element, bound by reading the logits and writing the
 // gradient.  A block takes kGradVecs vectors a thread of one row, so the row's
-// statistics are read once for 16 KB and the loads are in flight meanwhile.
+// statistics are read once for 8 KB and the loads are in flight meanwhile.
+// 4096 rows of 128256 bf16 logits take 317 us (6.6 TB/s); blocks of 256 threads
+// 321, of 512 453; 2 vectors a thread 392, 8 325.
 //   dx = 2^(lp log2 e) (A + B lp),  lp = x - lse, A = -(dlogp + dH H), B = -dH
 constexpr int kGradThreads = 128, kGradVecs = 4;
 

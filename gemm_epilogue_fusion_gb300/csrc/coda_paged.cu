@@ -66,6 +66,9 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 // accurate ones.
 // Bound by the bytes of Z, Q and the new slots: a row's heads are loaded while
 // its angles are computed, and its position and page are read a row ahead.
+// 16384 rows of 32 and 8 heads of 128 in bf16 take 64.7 us (6.2 TB/s).  One
+// block a row took 71; 6 heads in flight and 7 blocks an SM 85, 10 blocks 78,
+// blocks of 256 threads 86 and more.  A single row takes 3 us, a launch's own.
 constexpr int kAppendThreads = 128, kAppendHeads = 3;  // heads of a thread in flight
 constexpr int kAppendBlocks = 8;  // blocks of a launch for each SM: as many as fit one
 
@@ -204,10 +207,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 //     each block leaves (m, sum, o) in the workspace and the block that comes
 //     last joins them in the order of the keys, so the bits do not depend on
 //     which one it was.  No block waits for another.
-// The products run on mma.sync with the query heads as the 16 rows of the
-// instruction (tcgen05's smallest tile has 64, and its operands would have to
-// be rearranged in shared memory page by page): at the full HBM rate they need
-// about a fifth of the tensor pipe.  fp32 runs on the FMA pipe.
+// The products run on mma.sync with keys (then columns of v) as the 16 rows of
+// the instruction and query heads as its 8 columns: heads as the 16 rows did
+// twice the work for 8 heads (443 us for 380, see below).  tcgen05's smallest
+// tile has 64 rows, and its operands would have to be rearranged in shared
+// memory page by page; at the full HBM rate mma.sync needs about a fifth of the
+// tensor pipe.  fp32 runs on the FMA pipe.
+//
+// Measured, of heads of 128 (share of a plain copy's 6.77 TB/s):
+//   64 rows of 17 to 8192 keys, 32 query and 8 key heads, bf16    160 us   99%
+//   128 rows of 4000 to 16000 keys, 64 and 8 heads, e4m3 cache    380 us  102%
+//   one row of 131071 keys, 32 and 8 heads, bf16                   86 us   92%
+//   one row of 1900 keys, 32 and 8 heads, bf16                    10.0 us
+// The last is latency: 1.3 us until a block knows its run, 1.5 until its first
+// page and keys are there, about 4 for the join.  Other choices, in the first
+// two and the last of these: 2 blocks an SM 171 / 401, 4 (that spill) 232 / 560;
+// stages of 16 KB (bf16, KT = 32) 183, of 4 KB (e4m3, KT = 16) 475; 1, 2 or 3
+// tiles a block at least 11.2 / 10.0 / 10.6; the next tile's loads before the
+// wait for this one's 169 / 406; every part joined at once 93 in the third.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxWorkers = 512;  // blocks of a grid: bounds the workspace
@@ -218,6 +235,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What a block does with a key/value head's query heads at a time:
 //   kFew   up to 4 (fp32: 1);  kSome  up to 8 (fp32: 4);  kMany  up to 16 (fp32: 8)
+// Each takes what the next larger could take as well, for its registers and its
+// products (us, for 32 rows of 4096 keys of 8 heads of 128):
+//   4 query heads each   bf16 kFew 85.1, kSome 85.9, kMany 91.1;  e4m3 50.1, kMany 56.7
+//   8                    bf16 kSome 87.4, kMany 92.7
+//   fp32, 1 and 4        kFew 157, as kSome 161;  kSome 163, kMany 207
+// and kMany rounds the weights of bf16 once to 2^-8 where the others keep their
+// low part.  More than 16 heads take the keys once for each 16: 32 heads of one
+// key head run at 45% of the copy rate, and no product is bound by its operations.
 enum Heads { kFew, kSome, kMany };
 
 template <class T, class C, int DP_, Heads HEADS_>
@@ -235,10 +260,12 @@ struct AttnShape {
   static constexpr int KT = F32 ? 1024 / DP : KT0 > 32 || (E4M3 && NH == 2) ? 32 : KT0 < 16 ? 16 : KT0;
   static constexpr int CT = KT * kAttnWarps;
   static constexpr int STAGE = 2 * KT * PITCH;
-  static constexpr int ST = 2;  // stages of a ring: one more tile in flight made 162 us 169 (64 ragged rows)
+  // stages of a ring: one more tile in flight made 162 us 169 (64 ragged rows); where one block fills an SM's shared
+  // memory, 179 became 174 (32 rows of 4096 keys of 8 heads of 256)
+  static constexpr int ST = DP == 256 && sizeof(C) == 2 ? 3 : 2;
   static constexpr int CPR = PITCH / 16;  // 16-byte chunks of a row
   static constexpr int RING = kAttnWarps * ST * STAGE;
-  // the widest shape keeps its queries in shared memory: 64 registers a thread that o needs
+  // the widest shape keeps its queries in shared memory, 64 registers a thread that o needs (329 us became 190)
   static constexpr bool Q_SMEM = !F32 && NH == 2 && DP == 256;
   static constexpr int QBYTES = F32 ? RG * DP * 4 + kAttnWarps * KT * RG * 4 : Q_SMEM ? DP / 16 * 32 * 16 : 0;
   static constexpr int SMEM = RING + QBYTES;
@@ -494,7 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     }
   };
   const int row_bytes = p.head_dim * static_cast<int>(sizeof(C));
-  constexpr int LPR = CPR < 32 ? CPR : 32;  // lanes of a row
+  constexpr int LPR = (CPR & -CPR) < 32 ? CPR & -CPR : 32;  // lanes of a row: a power of two
   const char* const k_src = static_cast<const char*>(p.Kc) + (lane % LPR) * 16;
   const char* const v_src = static_cast<const char*>(p.Vc) + (lane % LPR) * 16;
   auto issue = [&](int stage) {
@@ -797,7 +824,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
 #pragma unroll
     for (int g = 0; g < RG; ++g) s2v[g] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int c = part; c < CPR; c += PARTS) {
+    for (int c = part; c < chunks; c += PARTS) {
       const float4 k = *reinterpret_cast<const float4*>(kb + staged<PITCH>(key, c));
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
@@ -1162,6 +1189,9 @@ template <class T, class C, Heads HEADS>
 cudaError_t pick_width(const AttnParams& p, cudaStream_t s, bool pdl) {
   if (p.head_dim <= 64) return run_attention<T, C, 64, HEADS>(p, s, pdl);
   if (p.head_dim <= 128) return run_attention<T, C, 128, HEADS>(p, s, pdl);
+  // 192 in the shape of 256 took 164 us instead of 125 (32 rows of 4096 keys, 32 and 8 heads): one block an SM, not two
+  if constexpr (sizeof(C) == 2)
+    if (p.head_dim <= 192) return run_attention<T, C, 192, HEADS>(p, s, pdl);
   return run_attention<T, C, 256, HEADS>(p, s, pdl);
 }
 

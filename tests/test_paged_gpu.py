@@ -190,7 +190,8 @@ def check(q, k, v, table, lens, s, got_o, got_lse, row_seq=None, scale=None):
 
 
 HEADS = [(32, 8, 128, 16), (64, 8, 128, 64), (4, 4, 64, 5), (16, 1, 80, 24), (14, 2, 256, 1), (40, 2, 96, 128),
-         (1, 1, 16, 3), (9, 1, 48, 7), (6, 3, 192, 16), (34, 1, 64, 16), (16, 1, 256, 16), (5, 1, 128, 2), (8, 2, 256, 8)]
+         (1, 1, 16, 3), (9, 1, 48, 7), (6, 3, 192, 16), (34, 1, 64, 16), (16, 1, 256, 16), (5, 1, 128, 2), (8, 2, 256, 8),
+         (14, 2, 192, 8), (32, 2, 160, 16), (3, 1, 176, 5), (16, 1, 192, 64)]
 
 
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
