@@ -70,13 +70,12 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 // block a row took 71; 6 heads in flight and 7 blocks an SM 85, 10 blocks 78,
 // blocks of 256 threads 86 and more.  A single row takes 3 us, a launch's own.
 constexpr int kAppendThreads = 128, kAppendHeads = 3;  // heads of a thread in flight
-constexpr int kAppendBlocks = 8;  // blocks of a launch for each SM: as many as fit one
 
 // What a row needs to know: its position (< 0: left out) and page.
 struct AppendRow {
   int pos, page;
 };
-__device__ __forceinline__ AppendRow append_row(const AppendParams& p, int64_t i, int64_t M) {
+__device__ __forceinline__ AppendRow append_row(const AppendParams& p, uint32_t i, uint32_t M) {
   AppendRow r = {-1, -1};
   if (i >= M) return r;
   r.pos = __ldg(p.positions + i);
@@ -91,8 +90,8 @@ __device__ __forceinline__ AppendRow append_row(const AppendParams& p, int64_t i
 template <class E, class C>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int VEC = 16 / sizeof(E);
-  const int chunks = p.head_dim / VEC, heads = p.q_heads + 2 * p.kv_heads, lanes = kAppendThreads / chunks;
-  const int c = threadIdx.x % chunks, h0 = threadIdx.x / chunks;
+  const int chunks = p.head_dim / VEC, heads = p.q_heads + 2 * p.kv_heads, lanes = p.lanes;
+  const int c = threadIdx.x % chunks, group = threadIdx.x / chunks, r0 = group / lanes, h0 = group - r0 * lanes;
   uint64_t turn[VEC / 2];
   if (p.rotate) {
     // by its generic address: the threads' chunks differ, and the constant cache serves one address at a time
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (h0 >= lanes) return;
+  if (r0 >= p.rows) return;
   float inv_k = 0.0f, inv_v = 0.0f, sk = 1.0f, sv = 1.0f;
   bool fast = true;
   if constexpr (sizeof(C) == 1) {
@@ -112,18 +111,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     inv_k = __frcp_rn(sk);
     inv_v = __frcp_rn(sv);
   }
-  AppendRow next = append_row(p, blockIdx.x, p.M);
-  for (int64_t i = blockIdx.x; i < p.M; i += gridDim.x) {
+  const uint32_t M = static_cast<uint32_t>(p.M), first = blockIdx.x * p.rows + r0;  // below 2^31, as a step is
+  AppendRow next = append_row(p, first, M);
+  for (uint32_t i = first; i < M; i += gridDim.x * p.rows) {
     const AppendRow row = next;
-    next = append_row(p, i + gridDim.x, p.M);
+    next = append_row(p, i + gridDim.x * p.rows, M);
     if (row.pos < 0) continue;
     if (row.page < 0 || row.page >= p.num_pages) {
-      if (threadIdx.x == 0) atomicOr(&g_paged_status, kDevBadIndex);
+      if (c == 0 && h0 == 0) atomicOr(&g_paged_status, kDevBadIndex);
       continue;
     }
     const int in_page = p.page_shift >= 0 ? row.pos & (p.page_size - 1) : row.pos % p.page_size;
-    const uint4* z = reinterpret_cast<const uint4*>(static_cast<const E*>(p.Z) + i * heads * p.head_dim) + c;
-    E* const q = static_cast<E*>(p.Q) + (p.Q ? i * p.q_heads * p.head_dim + c * VEC : 0);
+    const uint4* z = reinterpret_cast<const uint4*>(static_cast<const E*>(p.Z) + static_cast<int64_t>(i) * heads * p.head_dim) + c;
+    E* const q = static_cast<E*>(p.Q) + (p.Q ? static_cast<int64_t>(i) * p.q_heads * p.head_dim + c * VEC : 0);
     // elements of the caches before this row's slot of head 0
     const int64_t slot = (static_cast<int64_t>(row.page) * p.kv_heads * p.page_size + in_page) * p.head_dim + c * VEC;
     float s[VEC / 2], co[VEC / 2];
@@ -1214,10 +1214,27 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
   const void* k = f32    ? reinterpret_cast<const void*>(append_kernel<float, float>)
                   : e4m3 ? reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_fp8_e4m3>)
                          : reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_bfloat16>);
-  // about the blocks that fit the GPU at once, each with its share of the rows
-  const int64_t fit = static_cast<int64_t>(device_sm_count()) * kAppendBlocks;
-  const int64_t turns = (p.M + fit - 1) / fit, grid = (p.M + turns - 1) / turns;
-  void* args[] = {const_cast<AppendParams*>(&p)};
+  static std::atomic<int> fits[3];  // blocks that fit an SM, by type: 7 to 9
+  std::atomic<int>& fit = fits[f32 ? 2 : e4m3];
+  int blocks = fit.load(std::memory_order_relaxed);
+  if (blocks == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, k, kAppendThreads, 0);
+    if (e != cudaSuccess) return e;
+    if (blocks < 1) blocks = 1;
+    fit.store(blocks, std::memory_order_relaxed);
+  }
+  // rows that are short lie side by side in a block; no more blocks than fit the GPU at once, each with its share
+  AppendParams a = p;
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  a.lanes = kAppendThreads / (p.head_dim / (f32 ? 4 : 8));
+  a.rows = 1;
+  while (a.lanes % 2 == 0 && heads * 2 <= a.lanes * kAppendHeads) {
+    a.lanes /= 2;
+    a.rows *= 2;
+  }
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * blocks, all = (p.M + a.rows - 1) / a.rows;
+  const int64_t turns = (all + most - 1) / most, grid = (all + turns - 1) / turns;
+  void* args[] = {&a};
   return launch_ex(k, dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0, s, pdl, args);
 }
 
