@@ -171,7 +171,8 @@ struct AppendParams {
   int64_t M;
   int num_seqs, max_pages, q_heads, kv_heads, head_dim, num_pages, page_size;
   int page_shift;  // log2(page_size), or -1
-  int lanes, rows;  // heads of a row, and rows, that a block has in flight side by side
+  int lanes, rows;  // heads of a row, and rows, that a block has side by side
+  int parts;        // blocks that share a row's heads
   int rotate;
   // Pair j turns by turn[j] / 2^64 of a whole turn per position: base^(-2j/head_dim) / 2 pi
   uint64_t turn[kMaxHeadDim / 2];

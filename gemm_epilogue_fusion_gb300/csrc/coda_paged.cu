@@ -9,6 +9,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -91,7 +92,8 @@ template <class E, class C>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int VEC = 16 / sizeof(E);
   const int chunks = p.head_dim / VEC, heads = p.q_heads + 2 * p.kv_heads, lanes = p.lanes;
-  const int c = threadIdx.x % chunks, group = threadIdx.x / chunks, r0 = group / lanes, h0 = group - r0 * lanes;
+  const int c = threadIdx.x % chunks, group = threadIdx.x / chunks, r0 = group / lanes;
+  const int turn_of = blockIdx.x / p.parts, h0 = group - r0 * lanes + (blockIdx.x - turn_of * p.parts) * (lanes * kAppendHeads);
   uint64_t turn[VEC / 2];
   if (p.rotate) {
     // by its generic address: the threads' chunks differ, and the constant cache serves one address at a time
@@ -111,11 +113,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     inv_k = __frcp_rn(sk);
     inv_v = __frcp_rn(sv);
   }
-  const uint32_t M = static_cast<uint32_t>(p.M), first = blockIdx.x * p.rows + r0;  // below 2^31, as a step is
+  const uint32_t M = static_cast<uint32_t>(p.M), first = turn_of * p.rows + r0, step = gridDim.x / p.parts * p.rows;  // below 2^31, as a step is
   AppendRow next = append_row(p, first, M);
-  for (uint32_t i = first; i < M; i += gridDim.x * p.rows) {
+  for (uint32_t i = first; i < M; i += step) {
     const AppendRow row = next;
-    next = append_row(p, i + gridDim.x * p.rows, M);
+    next = append_row(p, i + step, M);
     if (row.pos < 0) continue;
     if (row.page < 0 || row.page >= p.num_pages) {
       if (c == 0 && h0 == 0) atomicOr(&g_paged_status, kDevBadIndex);
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     // elements of the caches before this row's slot of head 0
     const int64_t slot = (static_cast<int64_t>(row.page) * p.kv_heads * p.page_size + in_page) * p.head_dim + c * VEC;
     float s[VEC / 2], co[VEC / 2];
-    for (int hb = h0; hb < heads; hb += lanes * kAppendHeads) {
+    for (int hb = h0; hb < heads; hb += lanes * kAppendHeads * p.parts) {
       uint4 w[kAppendHeads];
 #pragma unroll
       for (int u = 0; u < kAppendHeads; ++u)
@@ -1232,10 +1234,13 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
     a.lanes /= 2;
     a.rows *= 2;
   }
+  // few rows of many heads: a block for each round of loads
   const int64_t most = static_cast<int64_t>(device_sm_count()) * blocks, all = (p.M + a.rows - 1) / a.rows;
   const int64_t turns = (all + most - 1) / most, grid = (all + turns - 1) / turns;
+  const int round = a.lanes * kAppendHeads;
+  a.parts = static_cast<int>(std::min<int64_t>((heads + round - 1) / round, most / grid));
   void* args[] = {&a};
-  return launch_ex(k, dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0, s, pdl, args);
+  return launch_ex(k, dim3(static_cast<unsigned>(grid * a.parts)), dim3(kAppendThreads), 0, s, pdl, args);
 }
 
 cudaError_t launch_paged_attention(const AttnParams& p, bool f32, bool e4m3, cudaStream_t s, bool pdl) {
