@@ -67,9 +67,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 // accurate ones.
 // Bound by the bytes of Z, Q and the new slots: a row's heads are loaded while
 // its angles are computed, and its position and page are read a row ahead.
-// 16384 rows of 32 and 8 heads of 128 in bf16 take 64.7 us (6.2 TB/s).  One
-// block a row took 71; 6 heads in flight and 7 blocks an SM 85, 10 blocks 78,
-// blocks of 256 threads 86 and more.  A single row takes 3 us, a launch's own.
+// 16384 rows of 32 and 8 heads of 128 take 66 us in bf16 (6.1 TB/s), 70 with an
+// e4m3 cache, whose conversions cost registers (7 blocks an SM, not 8).  One
+// block a row took 71; 6 heads in flight and 7 blocks an SM 85, 2 heads 71,
+// blocks of 256 threads 86 and more; prefetching the next row to L2 82.  A
+// single row takes 2.6 us, a launch's own.
 constexpr int kAppendThreads = 128, kAppendHeads = 3;  // heads of a thread in flight
 
 // What a row needs to know: its position (< 0: left out) and page.
@@ -1225,7 +1227,9 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
     if (blocks < 1) blocks = 1;
     fit.store(blocks, std::memory_order_relaxed);
   }
-  // rows that are short lie side by side in a block; no more blocks than fit the GPU at once, each with its share
+  // Rows that are short lie side by side in a block (16384 rows of 8 and 2 heads of 64: 11 us, 20.6 one by one), and
+  // there are no more blocks than fit the GPU at once, each with its share of the rows (8 an SM where 7 fit: 92 us, not
+  // 70).
   AppendParams a = p;
   const int heads = p.q_heads + 2 * p.kv_heads;
   a.lanes = kAppendThreads / (p.head_dim / (f32 ? 4 : 8));
@@ -1234,7 +1238,7 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
     a.lanes /= 2;
     a.rows *= 2;
   }
-  // few rows of many heads: a block for each round of loads
+  // few rows of many heads: a block for each round of loads (250 rows of 64 and 8 heads of 128: 5.0 us, 6.0 with one)
   const int64_t most = static_cast<int64_t>(device_sm_count()) * blocks, all = (p.M + a.rows - 1) / a.rows;
   const int64_t turns = (all + most - 1) / most, grid = (all + turns - 1) / turns;
   const int round = a.lanes * kAppendHeads;
