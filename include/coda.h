@@ -475,14 +475,18 @@ CODA_API coda_status coda_paged_append(const void* Z, const int32_t* positions, 
  *   scale   finite, > 0 (1 / sqrt(head_dim) as a rule)
  *   O       [M, q_heads * head_dim], dtype
  *   lse     nullable [M, q_heads] fp32: log sum_t exp(s_t)
- * Scores, the running maximum and sum, and the outputs are held in fp32.
+ * Scores, the running maximum and sum, and the outputs are held in fp32.  The
+ * weights that multiply the values are rounded: to bf16 plus a low part (bf16,
+ * q_heads / kv_heads <= 8; together exact to 2^-16), to bf16 (more heads), to
+ * f16 (an e4m3 cache), not at all (fp32).
  * A row without keys, or whose scores are all -inf, gives o = 0 and lse =
  * -inf.  Slots behind lengths[i] are never read into the result, whatever
  * they hold; NaN in a key or value of the row itself propagates.  M * q_heads < 2^31.
  * A row whose sequence is out of range counts as a row without keys, a length
  * beyond max_pages * page_size as that length, and keys on a page out of
  * range are left out; each raises the device status.
- * The same inputs give the same bits on every call on one device.
+ * The same inputs give the same bits on every call on one device; a row's last
+ * bits depend on the call's other lengths, which decide where it is split.
  * workspace: coda_paged_attention_workspace_bytes(q_heads, kv_heads,
  *   head_dim) bytes of device memory (the same for any M and lengths; -1 for
  *   heads out of range), zeroed by the caller before its first use; every call
