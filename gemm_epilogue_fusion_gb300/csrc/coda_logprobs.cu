@@ -317,32 +317,25 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
         }
       }
     };
-    if (CLUSTER && v1 - v0 <= U * NT) {  // one round of loads: an owner still has its elements
-      if (owner) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) collect(q[u], v0 + tid + u * NT < v1 ? v0 + tid + u * NT : vecs);
-      }
-    } else {
-      const uint32_t mask = __ballot_sync(0xffffffffu, owner);
-      int at = 0;
-      if (lane == 0 && mask != 0) at = atomicAdd(&sh.owners, __popc(mask));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
-      if (owner) sh.owner[at] = tid;
-      __syncthreads();
-      // the owners' vectors dealt to the threads, 2^shift an owner (a few more than it has)
-      const int mine = (v1 - v0 + NT - 1) / NT, shift = mine > 1 ? 32 - __clz(mine - 1) : 0, all = sh.owners << shift;
-      auto place = [&](int k) { return k < all ? v0 + sh.owner[k >> shift] + (k & ((1 << shift) - 1)) * NT : v1; };
-      int u = place(tid);
-      uint4 vec;
-      if (u < v1) vec = load_vec<E>(x, u, p.V);
-      warp_sums();  // while the elements are on their way
-      sums_done = true;
+    const uint32_t mask = __ballot_sync(0xffffffffu, owner);
+    int at = 0;
+    if (lane == 0 && mask != 0) at = atomicAdd(&sh.owners, __popc(mask));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
+    if (owner) sh.owner[at] = tid;
+    __syncthreads();
+    // the owners' vectors dealt to the threads, 2^shift an owner (a few more than it has)
+    const int mine = (v1 - v0 + NT - 1) / NT, shift = mine > 1 ? 32 - __clz(mine - 1) : 0, all = sh.owners << shift;
+    auto place = [&](int k) { return k < all ? v0 + sh.owner[k >> shift] + (k & ((1 << shift) - 1)) * NT : v1; };
+    int u = place(tid);
+    uint4 vec;
+    if (u < v1) vec = load_vec<E>(x, u, p.V);
+    warp_sums();  // while the elements are on their way
+    sums_done = true;
 #pragma unroll 1
-      for (int k = tid; k < all; k += NT) {
-        if (u < v1) collect(vec, u);
-        u = place(k + NT);
-        if (u < v1) vec = load_vec<E>(x, u, p.V);
-      }
+    for (int k = tid; k < all; k += NT) {
+      if (u < v1) collect(vec, u);
+      u = place(k + NT);
+      if (u < v1) vec = load_vec<E>(x, u, p.V);
     }
   }
   if (!sums_done) warp_sums();
@@ -474,24 +467,30 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
     if (tid == 0) sh.part = row;
     if (p.top > 0) {
       // an alternative's rank: those above it in each block's list, found by bisection by a lane for each list (the
-      // lists' number is a power of two)
-      const int n = ranks * p.top * ranks;
+      // lists' number is a power of two), two alternatives at a time
+      constexpr int SIDE = 2;
+      const int n = ranks * p.top * ranks, log2_ranks = 31 - __clz(ranks), half = 1 << (31 - __clz(p.top));
 #pragma unroll 1
-      for (int c = tid; c < ((n + 31) & ~31); c += NT) {
-        const int from = min(c, n - 1);
-        const uint64_t mine = sh.cand[from / ranks];
-        const uint64_t* list = sh.cand + (from & (ranks - 1)) * p.top;
-        int lo = 0, hi = p.top;
-#pragma unroll 1
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (list[mid] > mine)
-            lo = mid + 1;
-          else
-            hi = mid;
+      for (int c0 = tid; c0 < ((n + 31) & ~31); c0 += SIDE * NT) {
+        uint64_t mine[SIDE];
+        int list[SIDE], lo[SIDE];
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j) {
+          const int from = min(c0 + j * NT, n - 1);
+          mine[j] = sh.cand[from >> log2_ranks];
+          list[j] = (from & (ranks - 1)) * p.top - 1;
+          lo[j] = 0;
         }
-        for (int o = 1; o < ranks; o <<= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
-        if (c < n && (c & (ranks - 1)) == 0 && lo < p.top && mine != 0) sh.best[lo] = mine;
+#pragma unroll 1
+        for (int step = half; step > 0; step >>= 1)
+#pragma unroll
+          for (int j = 0; j < SIDE; ++j)
+            if (lo[j] + step <= p.top && sh.cand[list[j] + lo[j] + step] > mine[j]) lo[j] += step;
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j) {
+          for (int o = 1; o < ranks; o <<= 1) lo[j] += __shfl_xor_sync(0xffffffffu, lo[j], o);
+          if (c0 + j * NT < n && (c0 & (ranks - 1)) == 0 && lo[j] < p.top && mine[j] != 0) sh.best[lo[j]] = mine[j];
+        }
       }
     }
     __syncthreads();
@@ -614,16 +613,20 @@ cudaError_t run_logprobs(LogprobsParams p, int64_t M, int c, cudaStream_t s, boo
 //   few rows    64 x 16000: 6.0 / 4.7 / 4.7  200 x 16000: 6.4 / 5.3 / 5.9  400 x 8192: 5.3 / 5.4 / 7.9
 // so rows that leave SMs idle take 512 threads, many rows fewer while they are short: a row's serial end, which finds
 // its alternatives, then leaves more of the SM to other rows.
-// One row or a few that are long take a cluster: 1 x 128256 in 9.0 / 8.3 / 6.9 / 6.9 us by 1 / 2 / 4 / 8 blocks of 512,
-// 1 x 200000 in 13.0 / 10.0 / 8.1 / 7.1, but 1 x 50264 in 6.1 / 7.0 / 6.9 / 7.0 and 76 x 128256 in 9.4 by one and 8.7 by
-// two.  From 4.5 rounds of loads a row is split until a block has one round, or the blocks fill the SMs.
+// One row or a few that are long take a cluster (us by 1 / 2 / 4 / 8 blocks of 512, for 0, 8 and 50 alternatives):
+//   1 x 50264    4.6 / 4.7 / 4.0 / 4.0   6.1 / 6.9 / 6.3 / 6.7    8.2 / 8.3 / 7.8 / 9.8
+//   1 x 70000    5.5 / 5.2 / 4.5 / 4.0   7.1 / 7.4 / 6.7 / 6.6   10.1 / 9.4 / 8.3 / 9.8
+//   1 x 128256   7.3 / 5.9 / 4.6 / 4.0   8.8 / 8.0 / 6.9 / 6.6   12.1 / 10.0 / 8.5 / 9.7
+//   1 x 200000   10.5 / 7.7 / 5.8 / 4.8  12.2 / 9.8 / 8.0 / 7.3  16.8 / 12.9 / 10.2 / 10.6
+// and 76 x 128256 takes 9.4 by one and 8.8 by two (8 alternatives).  So from 3.5 rounds of loads a row is split until a
+// block has one round, or the blocks fill the SMs, by at most 8, or 4 where many alternatives have to be merged.
 template <class E>
 cudaError_t pick_logprobs(const LogprobsParams& p, int64_t M, cudaStream_t s, bool pdl) {
   constexpr int64_t ROUND = 512 * kRowVecs * (16 / sizeof(E));
   const int sms = device_sm_count();
   int c = 1;
-  if (p.V * 2 >= ROUND * 9)
-    while (c < kMaxCluster && M * c * 2 <= sms && p.V > ROUND * c) c *= 2;
+  if (p.V * 2 >= ROUND * 7)
+    while (c < (p.top > 16 ? kMaxCluster / 2 : kMaxCluster) && M * c * 2 <= sms && p.V > ROUND * c) c *= 2;
   if (c > 1) return run_logprobs<E, 512, true>(p, M, c, s, pdl);
   const int64_t bytes = static_cast<int64_t>(p.V) * sizeof(E);
   if (M <= 2 * sms || bytes > 128 * 1024) return run_logprobs<E, 512, false>(p, M, 1, s, pdl);

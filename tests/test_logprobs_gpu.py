@@ -51,7 +51,8 @@ def check_forward(x, targets, top):
 @pytest.mark.parametrize("M,V,top", [(1, 1, 1), (1, 1, 0), (3, 2, 2), (2, 7, 5), (5, 64, 64), (4, 100, 20), (1, 257, 3),
                                      (7, 1000, 1), (3, 4096, 50), (2, 8193, 64), (300, 515, 8), (1, 50257, 20),
                                      (5, 32000, 0), (160, 9999, 5), (1, 200001, 64), (20, 33001, 12),
-                                     (1, 73729, 20), (40, 90001, 12), (500, 9999, 5), (460, 25001, 3), (1500, 603, 8)])
+                                     (1, 73729, 20), (2, 57345, 64), (1, 57344, 16), (40, 90001, 12), (500, 9999, 5),
+                                     (460, 25001, 3), (1500, 603, 8)])
 def test_logprobs_against_64_bits(dt, M, V, top):
     g = U.gen(M * 7 + V)
     x = (torch.randn(M, V, generator=g) * 3).to(dt)
