@@ -159,7 +159,8 @@ struct LogprobsShared {
 // row, so their elements are read once more, from L2 as a rule: 20 of 512
 // threads are 4% of the row.  The few elements that reach the bound are ranked
 // by counting.  If ties leave more than kCandidates of them (512 to 2048 make
-// no difference otherwise), the alternatives are found one by one instead.
+// no difference otherwise), those at the bound are taken in the order of the
+// row, and if more than that are above it, one by one.
 //
 // Bound by the row's bytes.  bf16 costs about 5 issue slots an element (the
 // arithmetic is packed in pairs) of the 11 that the HBM rate leaves.  2048 rows
@@ -347,7 +348,60 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
     if (lane == 0) sh.part = a;
   }
   if (p.top > 0) {
-    const int n = sh.found;
+    int n = sh.found;
+    if (__builtin_expect(n > kCandidates, 0)) {
+      // many equal elements at the bound: those above it once more, then as many of the equal ones as are missing, in
+      // the order of the row
+      const uint32_t bound = sh.bound;
+      __syncthreads();
+      if (tid == 0) sh.found = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int u = v0 + tid; u < v1; u += NT) {
+        const uint4 vec = load_vec<E>(x, u, p.V);
+        const E* e = reinterpret_cast<const E*>(&vec);
+#pragma unroll
+        for (int z = 0; z < VEC; ++z) {
+          const uint32_t j = u * VEC + z, val = value_key(to_f32(e[z]));
+          if (val > bound && j < static_cast<uint32_t>(p.V)) {
+            const int at = atomicAdd(&sh.found, 1);
+            if (at < kCandidates) sh.cand[at] = (static_cast<uint64_t>(val) << 32) | static_cast<uint32_t>(~j);
+          }
+        }
+      }
+      __syncthreads();
+      n = sh.found;
+#pragma unroll 1
+      for (int first = v0; first < v1 && n < local; first += NT) {
+        const int u = first + tid;
+        uint4 vec;
+        uint32_t equal = 0;  // a bit for each
+        if (u < v1) {
+          vec = load_vec<E>(x, u, p.V);
+          const E* e = reinterpret_cast<const E*>(&vec);
+#pragma unroll
+          for (int z = 0; z < VEC; ++z)
+            equal |= (value_key(to_f32(e[z])) == bound && u * VEC + z < p.V ? 1u : 0u) << z;
+        }
+        int upto = __popc(equal);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += t;
+        }
+        if (lane == 31) sh.red[w] = upto;
+        __syncthreads();
+        int at = n + upto - __popc(equal), all = 0;
+        for (int o = 0; o < NT / 32; ++o) {
+          if (o < w) at += static_cast<int>(sh.red[o]);
+          all += static_cast<int>(sh.red[o]);
+        }
+        for (; equal != 0 && at < local; ++at, equal &= equal - 1)
+          sh.cand[at] = (static_cast<uint64_t>(bound) << 32) | static_cast<uint32_t>(~(u * VEC + __ffs(equal) - 1));
+        n = min(n + all, local);
+        __syncthreads();
+      }
+    }
     if (__builtin_expect(n <= kCandidates, 1)) {
       if (n <= 32) {
         const uint64_t all = lane < n ? sh.cand[lane] : 0u;

@@ -61,7 +61,7 @@ def test_logprobs_against_64_bits(dt, M, V, top):
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "few values", "blocks", "one large"])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "few values", "blocks", "one large", "few threads", "nan"])
 @pytest.mark.parametrize("M,V", [(2, 40000), (170, 6001), (100, 12001), (3, 100001), (500, 3001),
                                  (470, 13001)])
 def test_alternatives_in_hard_orders(dt, kind, M, V):
@@ -70,10 +70,20 @@ def test_alternatives_in_hard_orders(dt, kind, M, V):
     j = torch.arange(V, dtype=torch.float32).expand(M, V)
     x = {"equal": torch.full((M, V), -1.5), "rising": j / V * 8, "falling": -j / V * 8,
          "few values": torch.randint(0, 3, (M, V), generator=g).float(),
-         "blocks": (j // 97) % 11, "one large": torch.randn(M, V, generator=g)}[kind].clone()
+         "blocks": (j // 97) % 11, "one large": torch.randn(M, V, generator=g),
+         # thousands of elements above all others in one thread of six
+         "few threads": torch.where((j // 8) % 128 < 20, 100 - (j // 8) % 128, torch.randn(M, V, generator=g)),
+         "nan": j % 5}[kind].clone()
     if kind == "one large":
         x[:, V // 2] = 300.0
     t = torch.randint(0, V, (M,), generator=g, dtype=torch.int32)
+    if kind == "nan":
+        import gemm_epilogue_fusion_gb300 as gg
+        x[:, 50::2] = math.nan
+        got = gg.coda_logprobs(padded(x.to(dt)), t.cuda(), 33)
+        assert torch.isnan(got["lse"]).all()
+        assert (got["top_ids"].cpu() == torch.arange(50, 50 + 2 * 33, 2)).all()
+        return
     check_forward(x.to(dt), t, 33)
 
 
