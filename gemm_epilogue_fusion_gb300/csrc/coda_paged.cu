@@ -576,12 +576,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   constexpr int OW = S::F32 ? RG * DP / 32 : NH * DP / 4;
   constexpr int NR = S::F32 ? RG : 2 * NH;
   constexpr int KS = DP / 16;
-  // kFew, bf16: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to bf16;
-  // kSome, bf16: a second product does.  f16 weights (e4m3 caches) lose 2^-11, kMany rounds once (2^-8 at most).
-  // f16 weights are taken 2^15 times as large: 2^-29 of the largest is still a normal number, and what vanishes below
-  // 2^-40 of it is no 2^-20 of a row's sum in 10^6 keys.
+  // kFew: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to 16 bits; kSome, and
+  // e4m3 caches' kMany: a second product does.  bf16's kMany rounds once (2^-9).
+  // f16 weights (e4m3 caches) are taken 2^15 times as large: 2^-29 of the largest is still a normal number, and what
+  // vanishes below 2^-40 of it is no 2^-20 of a row's sum in 10^6 keys.
   constexpr float UP = F16 ? 15.0f : 0.0f;
-  constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && !F16 && HEADS == kSome;
+  constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && (F16 ? HEADS != kFew : HEADS == kSome);
   float o[OW], m[NR], l[NR];
   uint32_t q[S::F32 ? 1 : NH * KS * 2] = {};
   float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
     // o^T += v^T p^T: 16 columns by 8 heads a tile, 16 keys at a time
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      uint32_t b[NH][2], low[2];
+      uint32_t b[NH][2], low[NH][2];
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
             if constexpr (LOW_COLS)
               hi = lane & 2 ? lo : hi;
             else
-              low[hf] = transpose8x8(lo);
+              low[nh][hf] = transpose8x8(lo);
           }
           b[nh][hf] = transpose8x8(hi);
         }
@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
           for (int nh = 0; nh < NH; ++nh) {
             float(&acc)[4] = *reinterpret_cast<float(*)[4]>(o + (nh * (DP / 16) + d) * 4);
             mma16816<F16>(acc, a[0], a[1], a[2], a[3], b[nh][0], b[nh][1]);
-            if constexpr (LOW_MMA) mma16816<F16>(acc, a[0], a[1], a[2], a[3], low[0], low[1]);
+            if constexpr (LOW_MMA) mma16816<F16>(acc, a[0], a[1], a[2], a[3], low[nh][0], low[nh][1]);
           }
         }
       } else {
@@ -810,6 +810,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
             for (int nh = 0; nh < NH; ++nh) {
               float(&acc)[4] = *reinterpret_cast<float(*)[4]>(o + (nh * (DP / 16) + d + u) * 4);
               mma16816<F16>(acc, a0, a1, a2, a3, b[nh][0], b[nh][1]);
+              if constexpr (LOW_MMA) mma16816<F16>(acc, a0, a1, a2, a3, low[nh][0], low[nh][1]);
             }
           }
         }
@@ -1206,8 +1207,7 @@ cudaError_t pick_attention(const AttnParams& p, cudaStream_t s, bool pdl) {
     if (G == 1) return pick_width<T, C, kFew>(p, s, pdl);
     return G <= 4 ? pick_width<T, C, kSome>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
   } else {
-    if constexpr (sizeof(C) == 2)  // f16 weights need no second part: kFew is for bf16
-      if (G <= 4) return pick_width<T, C, kFew>(p, s, pdl);
+    if (G <= 4) return pick_width<T, C, kFew>(p, s, pdl);
     return G <= 8 ? pick_width<T, C, kSome>(p, s, pdl) : pick_width<T, C, kMany>(p, s, pdl);
   }
 }
