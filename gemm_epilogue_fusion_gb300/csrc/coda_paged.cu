@@ -244,8 +244,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 //   4 query heads each   bf16 kFew 85.1, kSome 85.9, kMany 91.1;  e4m3 50.1, kMany 56.7
 //   8                    bf16 kSome 87.4, kMany 92.7
 //   fp32, 1 and 4        kFew 157, as kSome 161;  kSome 163, kMany 207
-// and kMany rounds the weights of bf16 once to 2^-8 where the others keep their
-// low part.  More than 16 heads take the keys once for each 16: 32 heads of one
+// More than 16 heads take the keys once for each 16: 32 heads of one
 // key head run at 45% of the copy rate, and no product is bound by its operations.
 enum Heads { kFew, kSome, kMany };
 
@@ -576,12 +575,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
   constexpr int OW = S::F32 ? RG * DP / 32 : NH * DP / 4;
   constexpr int NR = S::F32 ? RG : 2 * NH;
   constexpr int KS = DP / 16;
-  // kFew: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to 16 bits; kSome, and
-  // e4m3 caches' kMany: a second product does.  bf16's kMany rounds once (2^-9).
+  // kFew: columns 4 to 7 repeat the heads and take what the weights lose when they are rounded to 16 bits; kSome and
+  // kMany: a second product does.
   // f16 weights (e4m3 caches) are taken 2^15 times as large: 2^-29 of the largest is still a normal number, and what
   // vanishes below 2^-40 of it is no 2^-20 of a row's sum in 10^6 keys.
   constexpr float UP = F16 ? 15.0f : 0.0f;
-  constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && (F16 ? HEADS != kFew : HEADS == kSome);
+  constexpr bool LOW_COLS = !S::F32 && HEADS == kFew, LOW_MMA = !S::F32 && HEADS != kFew;
   float o[OW], m[NR], l[NR];
   uint32_t q[S::F32 ? 1 : NH * KS * 2] = {};
   float s2[NR];  // scale log2 e (and the scales of an e4m3 cache's keys and of q)

@@ -476,9 +476,8 @@ CODA_API coda_status coda_paged_append(const void* Z, const int32_t* positions, 
  *   O       [M, q_heads * head_dim], dtype
  *   lse     nullable [M, q_heads] fp32: log sum_t exp(s_t)
  * Scores, the running maximum and sum, and the outputs are held in fp32.  The
- * weights that multiply the values are held in two 16-bit parts, together
- * exact to 2^-16 (f16 with an e4m3 cache, else bf16, where q_heads / kv_heads >
- * 8 are rounded once, to 2^-9); fp32 does not round them.
+ * weights that multiply the values are held in two 16-bit parts (f16 with an
+ * e4m3 cache, else bf16), together exact to 2^-16; fp32 does not round them.
  * A row without keys, or whose scores are all -inf, gives o = 0 and lse =
  * -inf.  Slots behind lengths[i] are never read into the result, whatever
  * they hold; NaN in a key or value of the row itself propagates.  M * q_heads < 2^31.

@@ -12,7 +12,8 @@ import decode_util as U
 from test_paged_gpu import BF, E4, make, scales
 
 LENS = [64, 1, 150, 0, 33]
-HEADS = {BF: [(4, 16), (3, 64), (8, 16), (5, 128), (7, 192), (6, 256)],
+HEADS = {BF: [(4, 16), (3, 64), (8, 16), (5, 128), (7, 192), (6, 256), (16, 16), (9, 64), (16, 128), (12, 192),
+              (16, 256), (32, 32)],
          E4: [(4, 16), (1, 64), (8, 16), (6, 128), (2, 192), (5, 256), (8, 128), (16, 16), (9, 64), (16, 128), (12, 192),
               (16, 256), (32, 32)]}
 CASES = [(ct, hq, d) for ct, heads in HEADS.items() for hq, d in heads]
