@@ -66,21 +66,29 @@ __device__ __forceinline__ float largest(const uint4 (&w)[N]) {
   }
 }
 
-// Logits of this size or more take the careful path: times log2 e they could
-// leave fp32's range.  A power of two that bf16 holds.
-constexpr float kHuge = 0x1p126f;
+// The pass takes x log2 e relative to a rounded base, whose rounding is at most
+// 1 while |x| < 2^24 (its weights are off by a factor within [1/2, 2], which is
+// taken out at the end) and grows with |x| without bound.  So
+//   - logits below -kLift are taken as -kLift;
+//   - a thread whose largest logit is kFar or more in size leaves its sums out;
+//   - a row (or a block's part of it) whose largest logit is kCareful or more in
+//     size is summed once more from the differences to it.
+// The steps between the three are far more than the 150 beyond which a weight
+// is 0, so what is lifted or left out has no weight beside a largest logit above
+// -kCareful.  Powers of two that bf16 holds.
+constexpr float kCareful = 0x1p23f, kFar = 0x1p24f, kLift = 0x1p25f;
 
-// 16 bytes of logits, none below -kHuge (NaN stays).
+// 16 bytes of logits, none below -kLift (NaN stays).
 template <class E>
 __device__ __forceinline__ uint4 lifted(const uint4& w) {
   uint4 o;
   if constexpr (sizeof(E) == 4) {
-    o = make_uint4(__float_as_uint(max_nan(__uint_as_float(w.x), -kHuge)), __float_as_uint(max_nan(__uint_as_float(w.y), -kHuge)),
-                   __float_as_uint(max_nan(__uint_as_float(w.z), -kHuge)), __float_as_uint(max_nan(__uint_as_float(w.w), -kHuge)));
+    o = make_uint4(__float_as_uint(max_nan(__uint_as_float(w.x), -kLift)), __float_as_uint(max_nan(__uint_as_float(w.y), -kLift)),
+                   __float_as_uint(max_nan(__uint_as_float(w.z), -kLift)), __float_as_uint(max_nan(__uint_as_float(w.w), -kLift)));
   } else {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
     __nv_bfloat162* r = reinterpret_cast<__nv_bfloat162*>(&o);
-    const __nv_bfloat162 low = __floats2bfloat162_rn(-kHuge, -kHuge);
+    const __nv_bfloat162 low = __floats2bfloat162_rn(-kLift, -kLift);
 #pragma unroll
     for (int e = 0; e < 4; ++e) r[e] = __hmax2_nan(h[e], low);
   }
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
   const int tgt = tid == 0 && rank == 0 ? p.targets[i] : -1;
 
   // This thread's running maximum m and sums relative to base = m log2 e, two of each side by side: d = x log2 e - base
-  // is one operation for two elements.  -inf and huge negative logits are lifted to -2^126, whose weight is 0 as well.
+  // is one operation for two elements.  -inf and huge negative logits are lifted to -kLift, whose weight is 0 as well.
   float m = -INFINITY, base = 0.0f;
   float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
   const int whole = min(v1, p.V / VEC);  // vectors without an end of the row inside
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
     const float big = largest<E, U>(q);
     if (!(big <= m)) {
       m = max_nan(m, big);
-      const float to = fminf(fmaxf(m, -kHuge), kHuge) * kLog2e, d = base - to, c = ex2_approx(d);
+      const float to = fminf(fmaxf(m, -kLift), kLift) * kLog2e, d = base - to, c = ex2_approx(d);
       // the first time there is nothing to scale (and c may be infinite); a weight of 0 ends what was summed
       const bool none = c == 0.0f || s2.x + s2.y == 0.0f;
       t2 = none ? make_float2(0.0f, 0.0f) : fmul2(ffma2(s2, make_float2(d, d), t2), make_float2(c, c));
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
   Sums a = {m, s2.x + s2.y, t2.x + t2.y};
   if (!(m < INFINITY)) {
     a.s = a.t = NAN;  // +inf or NaN
-  } else if (fabsf(m) >= kHuge) {
+  } else if (fabsf(m) >= kFar) {
     a.s = a.t = 0.0f;  // no weight beside an ordinary logit (and see `careful`)
   } else {
     const float off = fmaf(m, kLog2e, -base), c = ex2_approx(-off);
@@ -455,8 +463,8 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
     }
   }
   __syncthreads();
-  if (__builtin_expect(fabsf(sh.part.m) >= kHuge && fabsf(sh.part.m) < INFINITY, 0)) {
-    // careful: every logit is huge (a row of the type's lowest value), so d is taken from the difference
+  if (__builtin_expect(fabsf(sh.part.m) >= kCareful && fabsf(sh.part.m) < INFINITY, 0)) {
+    // careful: the largest logit is huge (a row of the type's lowest value), so d is taken from the difference
     const float top = sh.part.m;
     a = {top, 0.0f, 0.0f};
 #pragma unroll 1
