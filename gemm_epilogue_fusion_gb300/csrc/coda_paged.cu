@@ -712,7 +712,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
         }
       }
     }
-    // weights 2^(s2 s - m)
+    // weights 2^(s2 s - m).  The product is rounded before m is taken off it, so that the largest weight is 2^0: relative to
+    // a rounded m, one multiply-add would make it 2^(m's rounding), which scores of 10^7 and more carry out of range
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          const float2 v = fmul2(make_float2(s[nh][t][x], s[nh][t][x + 1]), make_float2(s2[2 * nh], s2[2 * nh + 1]));
+          s[nh][t][x] = v.x;
+          s[nh][t][x + 1] = v.y;
+        }
     if (mask != (KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u)) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -731,7 +742,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       for (int t = 0; t < MT; ++t) big[r] = fmaxf(big[r], fmaxf(s[r >> 1][t][r & 1], s[r >> 1][t][2 + (r & 1)]));
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], x));
-      big[r] *= s2[r];
       more |= big[r] > m[r];
     }
     if (__any_sync(0xffffffffu, more)) {
@@ -747,15 +757,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<E, C, DP, HEADS>::CTAS
       for (int i = 0; i < OW; ++i) o[i] *= c[i / (DP / 4) * 2 + (i & 1)];
     }
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float base = m[r] == -INFINITY ? 0.0f : m[r] - UP;
+    for (int nh = 0; nh < NH; ++nh) {
+      const float2 off = make_float2(m[2 * nh] == -INFINITY ? 0.0f : -m[2 * nh], m[2 * nh + 1] == -INFINITY ? 0.0f : -m[2 * nh + 1]);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float& v = s[r >> 1][t][2 * hf + (r & 1)];
-          v = ex2_approx(fmaf(v, s2[r], -base));
-          l[r] += v;
+        for (int x = 0; x < 4; x += 2) {
+          float2 v = fadd2(make_float2(s[nh][t][x], s[nh][t][x + 1]), off);
+          if constexpr (F16) v = fadd2(v, make_float2(UP, UP));
+          v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+          s[nh][t][x] = v.x;
+          s[nh][t][x + 1] = v.y;
+          l[2 * nh] += v.x;
+          l[2 * nh + 1] += v.y;
         }
     }
     // o^T += v^T p^T: 16 columns by 8 heads a tile, 16 keys at a time
