@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "coda_internal.h"
 #include "sm103_ptx.cuh"
@@ -589,7 +590,14 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
 // 4096 rows of 128256 bf16 logits take 317 us (6.6 TB/s); blocks of 256 threads
 // 321, of 512 453; 2 vectors a thread 392, 8 325.
 //   dx = 2^(lp log2 e) (A + B lp),  lp = x - lse, A = -(dlogp + dH H), B = -dH
+// From kFarLse on, fp32 rounds lse by more than 2^-10 and in the end loses log V
+// altogether (a row of the type's lowest value), and p with it.  Such a row's
+// blocks each sum its exp(x - lse), whose differences are exact, and write their
+// part once more with the logarithm `rest` off lp as well.  That comes behind
+// the ordinary pass, which it costs 1%: with `rest` in the pass, or the choice
+// ahead of it, 4096 rows took 326 to 338 us.
 constexpr int kGradThreads = 128, kGradVecs = 4;
+constexpr float kFarLse = 0x1p15f;
 
 template <class E>
 __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const __grid_constant__ LogprobsGradParams p) {
@@ -613,22 +621,24 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const _
   const float lse = p.lse[i], H = p.entropy ? p.entropy[i] : 0.0f;
   const bool empty = lse == -INFINITY;
   const float dl = p.dlogp && tgt >= 0 && !empty ? p.dlogp[i] : 0.0f, dh = p.dentropy && !empty ? p.dentropy[i] : 0.0f;
-  const float A = -(dl + dh * H), B = -dh;
-#pragma unroll
-  for (int u = 0; u < kGradVecs; ++u) {
-    const int v = v0 + u * kGradThreads;
-    if (v >= vecs) break;
+  const float B = -dh;
+  // the gradient of vector v with its logits; far: with `rest`
+  auto put = [&](auto far, int v, const uint4& logits, float A, float rest) {
     float2 f[8 / sizeof(E)];
-    pairs<E>(q[u], f);
+    pairs<E>(logits, f);
     float g[VEC];
 #pragma unroll
     for (int e = 0; e < VEC / 2; ++e) {
       const float2 lp = fadd2(f[e], make_float2(-lse, -lse));
       float2 pr;
       if constexpr (sizeof(E) == 4) {
-        pr = make_float2(expf(lp.x), expf(lp.y));
+        pr = decltype(far)::value ? make_float2(expf(lp.x - rest), expf(lp.y - rest)) : make_float2(expf(lp.x), expf(lp.y));
       } else {
-        const float2 d = fmul2(lp, make_float2(kLog2e, kLog2e));
+        float2 d;
+        if constexpr (decltype(far)::value)
+          d = ffma2(lp, make_float2(kLog2e, kLog2e), make_float2(-rest * kLog2e, -rest * kLog2e));
+        else
+          d = fmul2(lp, make_float2(kLog2e, kLog2e));
         pr = make_float2(ex2_approx(d.x), ex2_approx(d.y));
       }
       const float2 r = fmul2(pr, ffma2(make_float2(B, B), lp, make_float2(A, A)));
@@ -658,6 +668,35 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_backward_kernel(const _
       for (int e = 0; e < VEC; ++e)
         if (v * VEC + e < p.V) dx[v * VEC + e] = oe[e];
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    if (v0 + u * kGradThreads >= vecs) break;
+    put(std::false_type(), v0 + u * kGradThreads, q[u], -(dl + dh * H), 0.0f);
+  }
+  if (__builtin_expect(fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY, 0)) {
+    __shared__ float sums[kGradThreads / 32];
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int v = threadIdx.x; v < vecs; v += kGradThreads) {
+      float2 f[8 / sizeof(E)];
+      pairs<E>(load_vec<E>(x, v, p.V), f);
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) sum += ex2_approx((f[e].x - lse) * kLog2e) + ex2_approx((f[e].y - lse) * kLog2e);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kGradThreads / 32; ++w) sum += sums[w];
+    // no more than a rounding may lack; an lse of other logits than this row's is taken as it is
+    const float lacks = logf(sum), rest = fabsf(lacks) <= fabsf(lse) * 0x1p-23f ? lacks : 0.0f;
+#pragma unroll 1
+    for (int u = 0; u < kGradVecs; ++u)
+      if (v0 + u * kGradThreads < vecs)
+        put(std::true_type(), v0 + u * kGradThreads, load_vec<E>(x, v0 + u * kGradThreads, p.V), dh * rest - (dl + dh * H), rest);
   }
 }
 

@@ -523,7 +523,8 @@ CODA_API coda_status coda_logprobs(const void* logits, int64_t ld, const int32_t
 /* Gradient of coda_logprobs' logp and entropy with respect to the logits:
  *   dlogits_j = dlogp ([j = t] - p_j) - dentropy p_j (x_j - lse + entropy)
  *   lse, entropy: as coda_logprobs wrote them (entropy may be NULL without
- *            dentropy)
+ *            dentropy).  Where |lse| >= 2^15, whose rounding would show in p,
+ *            the row is summed once more for what lse lacks.
  *   dlogp, dentropy: nullable [M] fp32 upstream gradients (NULL = 0)
  *   dlogits  rows of V elements in the logits' type, ldd elements apart; the
  *            columns [V, ldd) are left as they are.  May not overlap logits.
