@@ -904,7 +904,7 @@ def coda_selftest_wait_timeout(timeout_ns: int, stream=None):
 
 
 def coda_get_device_status() -> int:
-    """Synchronise and read/clear the device status word; raises CodaError on a timeout."""
+    """Synchronise and read/clear the device status words; raises CodaError on a timeout or (next) a bad index."""
     st = load_library().coda_get_device_status()
     _check(st)
     return st

@@ -1035,12 +1035,14 @@ coda_status coda_get_device_status(void) {
   g_msg[0] = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  const unsigned s = coda::read_clear_status_bf16() | coda::read_clear_status_tf32() |
-                     coda::read_clear_status_e4m3() | coda::read_clear_status_aux() |
-                     coda::read_clear_status_paged() | coda::read_clear_status_logprobs();
-  if (s == ~0u) return fail(CODA_ERR_CUDA, "could not read the device status word");
-  if (s & 1u) return fail(CODA_ERR_TIMEOUT, "a kernel gave up on a bounded wait (timeout)");
-  if (s & 2u)
+  const unsigned waits = coda::read_clear_status_bf16() | coda::read_clear_status_tf32() |
+                         coda::read_clear_status_e4m3() | coda::read_clear_status_aux();
+  if (waits == ~0u) return fail(CODA_ERR_CUDA, "could not read the device status word");
+  // the words of the other kernels, whose finding is another, are left for the next call
+  if (waits & 1u) return fail(CODA_ERR_TIMEOUT, "a kernel gave up on a bounded wait (timeout)");
+  const unsigned indices = coda::read_clear_status_paged() | coda::read_clear_status_logprobs();
+  if (indices == ~0u) return fail(CODA_ERR_CUDA, "could not read the device status word");
+  if (indices & 2u)
     return fail(CODA_ERR_INVALID_ARG, "a page, sequence, length or token index on the device was out of range");
   return CODA_OK;
 }

@@ -565,7 +565,8 @@ CODA_API coda_status coda_selftest_wait_timeout(int64_t timeout_ns, cudaStream_t
  * word: CODA_ERR_TIMEOUT if any kernel since the last call gave up on a
  * bounded wait, CODA_ERR_INVALID_ARG if one met an index out of range in
  * device memory (the paged cache and log-probability calls), CODA_ERR_CUDA if
- * the device reports an error, else CODA_OK. */
+ * the device reports an error, else CODA_OK.  Of both findings the timeout comes
+ * first, and the index with the next call. */
 CODA_API coda_status coda_get_device_status(void);
 
 #ifdef __cplusplus
