@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "coda.h"
+#include "coda_decode.h"
 #include "coda_internal.h"
 
 namespace coda {

@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "coda_decode.h"
 #include "coda_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -24,6 +25,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The two halves of cluster_sync, for work between them.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The larger of two values, NaN if one of them is.
 __device__ __forceinline__ float max_nan(float a, float b) {

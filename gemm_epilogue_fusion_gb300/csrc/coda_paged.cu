@@ -14,6 +14,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "coda_decode.h"
 #include "coda_internal.h"
 #include "fp8_e4m3.cuh"
 #include "sm103_ptx.cuh"

@@ -20,7 +20,6 @@ namespace coda {
 // Device status bits, OR-ed into the status word of the kernel's translation
 // unit and read back (and cleared) by coda_get_device_status().
 constexpr unsigned kDevTimeout = 1u;
-constexpr unsigned kDevBadIndex = 2u;  // a page, sequence or token index read on the device was out of range
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -144,12 +143,6 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-
-// The two halves of cluster_sync, for work between them.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Shared::cluster address of the same shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t cta_addr, uint32_t rank) {

@@ -93,3 +93,15 @@ def test_chain_bytes_of_the_8b_chain():
     # the first block's share equals the timed kernel's bytes
     w = WORKLOADS["llama8b_chain"]
     assert bench.timed_kernel_bytes(w, "block", 32) < fused
+
+
+def test_the_hashed_sources_hold_nothing_of_other_kernels():
+    """Recorded figures of the GEMM and auxiliary kernels are valid while those sources stay the same, so the decode and
+    scoring kernels' declarations are not among them."""
+    csrc = os.path.join(bench.ROOT, "gemm_epilogue_fusion_gb300", "csrc")
+    for files in bench.KERNEL_SOURCES.values():
+        for f in files:
+            text = open(os.path.join(csrc, f), encoding="utf-8").read()
+            for word in ("AppendParams", "AttnParams", "LogprobsParams", "LogprobsGradParams", "kDevBadIndex", "kMaxTop",
+                         "kMaxHeadDim", "launch_paged", "launch_logprobs"):
+                assert word not in text, (f, word)
