@@ -25,6 +25,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -125,8 +126,13 @@ def _load_marshal(lib) -> None:
     """The C marshalling of the short calls (coda_marshal.c), given the library's own entry points."""
     global _fast
     if _raw_stream is None or not os.path.exists(_build.MARSHAL):
-        return  # a PyTorch without CUDA: the checks in Python serve
-    from . import _coda_marshal as m
+        return  # a PyTorch without CUDA, or a module that was not built: the checks in Python serve
+    try:
+        from . import _coda_marshal as m
+    except ImportError as e:
+        warnings.warn(f"{_build.MARSHAL} cannot be loaded, the decode and scoring calls take longer on the host: {e}",
+                      RuntimeWarning, stacklevel=3)
+        return
     names = ("coda_paged_append", "coda_paged_attention", "coda_paged_attention_workspace_bytes", "coda_logprobs",
              "coda_logprobs_backward")
     m.init(torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.cuda.current_device,
