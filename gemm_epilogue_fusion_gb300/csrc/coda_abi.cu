@@ -1147,7 +1147,9 @@ coda_status coda_paged_append(const void* Z, const int32_t* positions, const int
   p.rotate = base != 0.0;
   if (p.rotate) {
     // base^(-2j / head_dim) / 2 pi < 1 as a 64-bit fraction of a turn, by repeated products in 64 bits: the
-    // relative error of term j is j 2^-53, so the turn count at position 2^31 is off by less than 1e-6 of a turn
+    // relative error of term j is j 2^-52 (the ratio's rounding and the products'), so the turn count at position 2^31
+    // is off by j base^(-2j / head_dim) 2^-21 / 2 pi: less than 4e-7 of a turn from base 10000 on, and less than 1e-5
+    // for any base (127 of 128 pairs in, at a base near 1)
     const double ratio = std::pow(base, -2.0 / static_cast<double>(head_dim));
     double f = 0.15915494309189535 * 0x1p64;
     for (int64_t j = 0; j < head_dim / 2; ++j, f *= ratio) p.turn[j] = static_cast<uint64_t>(f);
