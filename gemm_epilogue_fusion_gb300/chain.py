@@ -263,14 +263,24 @@ def decode_layer(Z, R, positions, lengths, page_table, k_cache, v_cache, q_heads
     return {**full_chain(a["o"], Wot, R, Wgt_f, Wut_f, Wdt, Wqt_f, eps, bufs, fused_reduce=True), **a}
 
 
+def _vocab(vocab: Optional[int], width: int) -> int:
+    """The number of tokens of a head of ``width`` rows."""
+    if vocab is None:
+        return width
+    if not 1 <= vocab <= width:
+        raise ValueError(f"vocab = {vocab} out of range [1, {width}], the head's rows")
+    return vocab
+
+
 def head_logprobs(h, P, Wvt_f, eps: float, targets, top: int = 0, vocab: Optional[int] = None,
                   bufs: Optional[dict] = None) -> dict:
     """The LM head on the residual stream h and its partials P (as coda_gemm_residual_partial_rms wrote them):
     logits = RMSNorm(h) Wv, then log probabilities of ``targets`` with entropy, lse and the ``top`` best alternatives.
     ``vocab``: the number of tokens when Wvt_f has padded rows behind them.  Returns coda_logprobs' dict and logits, r."""
     from . import coda_logprobs
+    V = _vocab(vocab, Wvt_f.shape[0])
     logits, r = _rowscale(h, Wvt_f, P, eps, bufs, "r", "logits", True)
-    got = coda_logprobs(logits if vocab is None else logits[:, :vocab], targets, top,
+    got = coda_logprobs(logits[:, :V], targets, top,
                         **{k: _b(bufs, k) for k in ("logp", "entropy", "lse", "top_logp", "top_ids")})
     return {**got, "logits": logits, "r": r}
 
@@ -281,7 +291,7 @@ def head_logprobs_backward(h, Wvt, gamma, fwd: dict, targets, dlogp=None, dentro
     head weight, ``fwd`` what head_logprobs returned."""
     from . import coda_gemm, coda_gemm_grad_norm, coda_logprobs_backward, coda_rmsnorm_backward
     logits = fwd["logits"]
-    V = logits.shape[1] if vocab is None else vocab
+    V = _vocab(vocab, logits.shape[1])
     # the padded tokens' columns take part in no softmax: their gradient is 0
     dlogits = torch.empty_like(logits) if V == logits.shape[1] else torch.zeros_like(logits)
     coda_logprobs_backward(logits[:, :V], targets, fwd["lse"], fwd["entropy"], dlogp, dentropy, dlogits[:, :V])
