@@ -480,7 +480,9 @@ CODA_API coda_status coda_paged_append(const void* Z, const int32_t* positions, 
  * e4m3 cache, else bf16), together exact to 2^-16; fp32 does not round them.
  * A row without keys, or whose scores are all -inf, gives o = 0 and lse =
  * -inf.  Slots behind lengths[i] are never read into the result, whatever
- * they hold; NaN in a key or value of the row itself propagates.  M * q_heads < 2^31.
+ * they hold; NaN in a key or value of the row itself propagates, and an
+ * infinite value makes its column infinite or NaN.  Values are summed before the
+ * division: sum_t |v_t| of a row stays below 2^127.  M * q_heads < 2^31.
  * A row whose sequence is out of range counts as a row without keys, a length
  * beyond max_pages * page_size as that length, and keys on a page out of
  * range are left out; each raises the device status.
