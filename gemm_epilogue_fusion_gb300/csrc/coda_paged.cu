@@ -63,13 +63,16 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 // cosines of its pairs are computed once a row.  The angle of pair j at
 // position pos is the fraction of a turn turn[j] * pos / 2^64, an exact product
 // that wraps by whole turns by itself; its upper 32 bits go to fp32 (2^-25 of
-// half a turn).  bf16 takes the sine and cosine of the special-function unit
-// (2^-21 of 1 on this range, a 32nd of the output's rounding), fp32 the
-// accurate ones.
+// half a turn).  Rows stored in bf16 take the sine and cosine of the
+// special-function unit (2^-21 of 1 on this range; the output's rounding is
+// 2^-9), fp32 the accurate ones, and so do e4m3 caches: an error that moves a
+// value over the middle of two codes costs a whole step, and the fast ones moved
+// 82 of 10^7 keys, these 13 (exact angles in fp32 arithmetic: 11).
 // Bound by the bytes of Z, Q and the new slots: a row's heads are loaded while
 // its angles are computed, and its position and page are read a row ahead.
-// 16384 rows of 32 and 8 heads of 128 take 66 us in bf16 (6.1 TB/s), 70 with an
-// e4m3 cache, whose conversions cost registers (7 blocks an SM, not 8).  One
+// 16384 rows of 32 and 8 heads of 128 take 66 us in bf16 (6.1 TB/s; the accurate
+// sines would make it 70), 74 with an e4m3 cache (70 with the fast ones), whose
+// conversions cost registers (7 blocks an SM, not 8), 126 in fp32.  One
 // block a row took 71; 6 heads in flight and 7 blocks an SM 85, 2 heads 71,
 // blocks of 256 threads 86 and more; prefetching the next row to L2 82.  A
 // single row takes 2.6 us, a launch's own.
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         for (int e = 0; e < VEC / 2; ++e) {
           const int t = static_cast<int>((turn[e] * static_cast<uint64_t>(row.pos)) >> 32);
           const float half_turns = static_cast<float>(t) * 0x1p-31f;
-          if constexpr (sizeof(E) == 4)
+          if constexpr (sizeof(E) == 4 || sizeof(C) == 1)
             sincospif(half_turns, &s[e], &co[e]);
           else
             __sincosf(half_turns * 3.14159265358979f, &s[e], &co[e]);
