@@ -181,7 +181,7 @@ struct LogprobsShared {
 // Bound by the row's bytes.  bf16 costs about 5 issue slots an element (the
 // arithmetic is packed in pairs) of the 11 that the HBM rate leaves.  2048 rows
 // of 128256 bf16 logits take 82 us without alternatives (6.4 TB/s), 92 with 8
-// (5.7 TB/s), 99 with 20 and 124 with 64: the end of a row costs its block
+// (5.7 TB/s), 101 with 20 and 128 with 64: the end of a row costs its block
 // about as long as 1 / 8 of the row.  kRowVecs of 2 / 3 / 4 / 6 made that
 // 102 / 98 / 92 / 103; a ring of cp.async stages that ran across the rows 130;
 // the bound found by bits over all warps 106.
@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
   };
 
   // ---- the bound of the alternatives: each warp's `each` largest keys (taken out one by one), of all of those the
-  // top-th.  top threads reach it, and with one or two more a warp than top needs few others do.
+  // top-th.  top threads reach it, and with one or two more a warp than top needs few others do.  (A last warp with few
+  // elements counts as a whole one: from 30 alternatives on, rows of 1025 to 1552 bf16 logits may gather fewer than top
+  // keys.  The bound is 0 then and every element reaches it: 300 rows of 1032 with 50 take 100 us, of 1000 8 us.)
   if (p.top > 0) {
     const int warps = max(min(NT / 32, (v1 - v0 + 31) / 32), 1);  // that have elements
     const int each = min(warps == NT / 32 ? (p.top + NT / 32 - 1) / (NT / 32) + 1 : (p.top + warps - 1) / warps + 1, 32);
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(NT, CLUSTER ? 2 : 1536 / NT) logprobs_kernel(c
 // Gradient: element by element, bound by reading the logits and writing the
 // gradient.  A block takes kGradVecs vectors a thread of one row, so the row's
 // statistics are read once for 8 KB and the loads are in flight meanwhile.
-// 4096 rows of 128256 bf16 logits take 317 us (6.6 TB/s); blocks of 256 threads
+// 4096 rows of 128256 bf16 logits take 320 us (6.6 TB/s); blocks of 256 threads
 // 321, of 512 453; 2 vectors a thread 392, 8 325.
 //   dx = 2^(lp log2 e) (A + B lp),  lp = x - lse, A = -(dlogp + dH H), B = -dH
 // From kFarLse on, fp32 rounds lse by more than 2^-10 and in the end loses log V

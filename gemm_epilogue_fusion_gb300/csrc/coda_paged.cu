@@ -72,7 +72,7 @@ __device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(E)]) {
 // its angles are computed, and its position and page are read a row ahead.
 // 16384 rows of 32 and 8 heads of 128 take 66 us in bf16 (6.1 TB/s; the accurate
 // sines would make it 70), 74 with an e4m3 cache (70 with the fast ones), whose
-// conversions cost registers (7 blocks an SM, not 8), 126 in fp32.  One
+// conversions and sines cost registers (6 blocks an SM, not 8), 126 in fp32.  One
 // block a row took 71; 6 heads in flight and 7 blocks an SM 85, 2 heads 71,
 // blocks of 256 threads 86 and more; prefetching the next row to L2 82.  A
 // single row takes 2.6 us, a launch's own.
@@ -220,16 +220,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // twice the work for 8 heads (443 us for 380, see below).  tcgen05's smallest
 // tile has 64 rows, and its operands would have to be rearranged in shared
 // memory page by page; at the full HBM rate mma.sync keeps the tensor pipe busy
-// for 9% (bf16) and 19% (e4m3) of the time.  fp32 runs on the FMA pipe.
+// for 9% (bf16) and 28% (e4m3) of the time.  fp32 runs on the FMA pipe.
 //
 // Measured, of heads of 128 (share of a plain copy's 6.77 TB/s):
-//   64 rows of 17 to 8192 keys, 32 query and 8 key heads, bf16    160 us   99%
-//   128 rows of 4000 to 16000 keys, 64 and 8 heads, e4m3 cache    380 us  102%
-//   one row of 131071 keys, 32 and 8 heads, bf16                   86 us   92%
+//   64 rows of 17 to 8192 keys, 32 query and 8 key heads, bf16    162 us   98%
+//   128 rows of 4000 to 16000 keys, 64 and 8 heads, e4m3 cache    387 us  100%
+//   one row of 131071 keys, 32 and 8 heads, bf16                   88 us   90%
 //   one row of 1900 keys, 32 and 8 heads, bf16                    10.0 us
 // The last is latency: 1.3 us until a block knows its run, 1.5 until its first
 // page and keys are there, about 4 for the join.  Other choices, in the first
-// two and the last of these: 2 blocks an SM 171 / 401, 4 (that spill) 232 / 560;
+// two and the last of these (when they took 160, 380 and 10.0): 2 blocks an SM 171 / 401, 4 (that spill) 232 / 560;
 // stages of 16 KB (bf16, KT = 32) 183, of 4 KB (e4m3, KT = 16) 475; 1, 2 or 3
 // tiles a block at least 11.2 / 10.0 / 10.6; the next tile's loads before the
 // wait for this one's 169 / 406; every part joined at once 93 in the third.
@@ -245,11 +245,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 //   kFew   up to 4 (fp32: 1);  kSome  up to 8 (fp32: 4);  kMany  up to 16 (fp32: 8)
 // Each takes what the next larger could take as well, for its registers and its
 // products (us, for 32 rows of 4096 keys of 8 heads of 128):
-//   4 query heads each   bf16 kFew 85.1, kSome 85.9, kMany 91.1;  e4m3 50.1, kMany 56.7
-//   8                    bf16 kSome 87.4, kMany 92.7
+//   4 query heads each   bf16 kFew 86.0, kSome 86.1, kMany 92.7;  e4m3 50.4, 50.8, 62.6
+//   8                    bf16 kSome 87.0, kMany 94.2;  e4m3 52.5, 63.9
+//   16                   bf16 kMany 96.8;  e4m3 68.7
 //   fp32, 1 and 4        kFew 157, as kSome 161;  kSome 163, kMany 207
-// More than 16 heads take the keys once for each 16: 32 heads of one
-// key head run at 45% of the copy rate, and no product is bound by its operations.
+// More than 16 heads take the keys once for each 16: 32 heads of one key head
+// run at 44% of the copy rate, 33% with an e4m3 cache.
 enum Heads { kFew, kSome, kMany };
 
 template <class T, class C, int DP_, Heads HEADS_>
@@ -1235,7 +1236,7 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
   const void* k = f32    ? reinterpret_cast<const void*>(append_kernel<float, float>)
                   : e4m3 ? reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_fp8_e4m3>)
                          : reinterpret_cast<const void*>(append_kernel<__nv_bfloat16, __nv_bfloat16>);
-  static std::atomic<int> fits[3];  // blocks that fit an SM, by type: 7 to 9
+  static std::atomic<int> fits[3];  // blocks that fit an SM, by type: 6 to 9
   std::atomic<int>& fit = fits[f32 ? 2 : e4m3];
   int blocks = fit.load(std::memory_order_relaxed);
   if (blocks == 0) {
@@ -1245,8 +1246,8 @@ cudaError_t launch_paged_append(const AppendParams& p, bool f32, bool e4m3, cuda
     fit.store(blocks, std::memory_order_relaxed);
   }
   // Rows that are short lie side by side in a block (16384 rows of 8 and 2 heads of 64: 11 us, 20.6 one by one), and
-  // there are no more blocks than fit the GPU at once, each with its share of the rows (8 an SM where 7 fit: 92 us, not
-  // 70).
+  // there are no more blocks than fit the GPU at once, each with its share of the rows (one an SM more, for an e4m3 cache:
+  // 92 us, not 70).
   AppendParams a = p;
   const int heads = p.q_heads + 2 * p.kv_heads;
   a.lanes = kAppendThreads / (p.head_dim / (f32 ? 4 : 8));
