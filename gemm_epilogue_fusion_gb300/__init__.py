@@ -1060,7 +1060,8 @@ def coda_route_backward(logits, ids, weights, dweights, *, renormalize: bool = T
 
 def coda_expert_dispatch(X, slots, *, scale=None, Xs=None, scale_s=None, T: Optional[int] = None, stream=None):
     """Xs[slots[i, j]] = X[i] for X [M, N] (fp32, bf16 or e4m3 bytes), and scale_s[slots[i, j]] = scale[i] when ``scale``
-    [M] is given.  ``T``: rows of Xs, M top_k unless given (or Xs is).  Returns (Xs [T, N], scale_s [T] or None)."""
+    [M] is given.  ``T``: rows of Xs, M top_k unless given (or Xs is).  Returns (Xs [T, N], scale_s [T], or None without
+    ``scale``: a given ``scale_s`` is then left as it is)."""
     lib = load_library()
     M, N = _matrix(X, "X")
     k = _matrix(slots, "slots")[1]
@@ -1069,8 +1070,7 @@ def coda_expert_dispatch(X, slots, *, scale=None, Xs=None, scale_s=None, T: Opti
     elif T is None:
         T = M * k
     Xs = _alloc(Xs, (T, N), X.dtype, X)
-    if scale is not None:
-        scale_s = _alloc(scale_s, (T,), torch.float32, X)
+    scale_s = None if scale is None else _alloc(scale_s, (T,), torch.float32, X)  # without scale it is not written
     if _fast is not None and _done(_fast.expert_dispatch(X, slots, scale, Xs, scale_s, _stream_arg(stream))):
         return Xs, scale_s
     code = _dtype_code(X)
@@ -1079,8 +1079,7 @@ def coda_expert_dispatch(X, slots, *, scale=None, Xs=None, scale_s=None, T: Opti
     _want(scale, "scale", (M,), _F32)
     _want(scale_s, "scale_s", (T,), _F32)
     _check(lib.coda_expert_dispatch(_dev(X, "X"), _dev(scale, "scale"), _dev(slots, "slots"), _dev(Xs, "Xs"),
-                                    _dev(scale_s, "scale_s") if scale is not None else None, M, N, k, T, code,
-                                    _stream(X, stream)))
+                                    _dev(scale_s, "scale_s"), M, N, k, T, code, _stream(X, stream)))
     return Xs, scale_s
 
 

@@ -317,7 +317,8 @@ def expert_layer(X, slots, offsets, weights, Wgut, Wdt, R=None, *, scale_x=None,
     (X and scale_x from coda_add_rmsnorm's q and scale, weights with scale_wgu and scale_wd [E]) in 5, act being
     quantised row by row.  ``save`` keeps G || U for the backward; ``want_p`` adds h's partial sums of squares P, for
     the next layer's coda_gemm_*_fused_rms.  Returns xs, act, y (rows in expert order), h and what was asked for."""
-    xs, sxs = coda_expert_dispatch(X, slots, scale=scale_x, Xs=_b(bufs, "xs"), scale_s=_b(bufs, "sxs"))
+    xs, sxs = coda_expert_dispatch(X, slots, scale=scale_x, Xs=_b(bufs, "xs"),
+                                   scale_s=_b(bufs, "sxs") if scale_x is not None else None)
     act, GU = coda_grouped_gemm_swiglu(xs, Wgut, offsets, row_scale=sxs, w_scale=scale_wgu, Act=_b(bufs, "act"),
                                        GU=_b(bufs, "GU") if save else None, save=save)
     out = {"xs": xs, "sxs": sxs, "act": act, "GU": GU}
