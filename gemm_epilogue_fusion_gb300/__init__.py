@@ -915,13 +915,15 @@ def coda_add_rmsnorm(X, gamma, eps: float, R=None, *, H=None, Y=None, Yq=None, s
     """h = X + R, r = 1 / sqrt(mean h^2 + eps), y = h r gamma, in X's type (``want_y`` or a given ``Y``), in e4m3 with a
     scale for each row (``want_q`` or a given ``Yq``), or both; without ``want_y``, y is wanted unless a ``Yq`` is given.
     X and R [M, N] may be strided views of rows.  Returns a dict: h (X itself without R, unless ``H`` is given), y, q,
-    scale [M], r [M]; what was not asked for is None."""
+    scale [M] (with q alone), r [M]; what was not asked for is None."""
     lib = load_library()
     if Y is None and (Yq is None if want_y is None else want_y):
         Y = torch.empty(_matrix(X, "X"), dtype=X.dtype, device=X.device)
     if Yq is None and want_q:
         Yq = torch.empty(_matrix(X, "X"), dtype=torch.uint8, device=X.device)
-    if Yq is not None and scale is None:
+    if Yq is None:
+        scale = None  # it is written with the codes alone
+    elif scale is None:
         scale = torch.empty(_matrix(X, "X")[0], dtype=torch.float32, device=X.device)
     if H is None and R is not None:
         H = torch.empty(_matrix(X, "X"), dtype=X.dtype, device=X.device)
@@ -942,8 +944,8 @@ def coda_add_rmsnorm(X, gamma, eps: float, R=None, *, H=None, Y=None, Yq=None, s
     x, ldx = _logits_rows(X, "X")
     res, ldr = (None, 0) if R is None else _logits_rows(R, "R")
     _check(lib.coda_add_rmsnorm(x, ldx, res, ldr, _dev(gamma, "gamma"), float(eps), _dev(H, "H"), _dev(Y, "Y"),
-                                _dev(Yq, "Yq"), _dev(scale, "scale") if Yq is not None else None, _dev(r, "r"), M, N,
-                                _dtype_code(X), _stream(X, stream)))
+                                _dev(Yq, "Yq"), _dev(scale, "scale"), _dev(r, "r"), M, N, _dtype_code(X),
+                                _stream(X, stream)))
     return out
 
 

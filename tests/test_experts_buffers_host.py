@@ -61,3 +61,14 @@ def test_an_e4m3_layer_uses_it(recorder):
     out = chain.expert_layer(X, slots, torch.zeros(5, dtype=I32), torch.ones(3, 2), Wgu, Wd, scale_x=torch.ones(3),
                              scale_wgu=one, scale_wd=one, bufs={"sxs": sxs})
     assert out["sxs"] is sxs and recorder.args("grouped_swiglu")[0][3] is sxs
+
+
+def test_the_norm_returns_no_scale_that_it_has_not_written(recorder):
+    X, stale = torch.zeros(3, 16, dtype=BF), torch.full((3,), 9.0)
+    got = g.coda_add_rmsnorm(X, torch.ones(16), 1e-5, scale=stale)
+    assert got["q"] is None and got["scale"] is None
+    assert recorder.args("add_rmsnorm")[0][6] is None
+    got = g.coda_add_rmsnorm(X, torch.ones(16), 1e-5, scale=stale, want_q=True)
+    assert got["scale"] is stale
+    codes = torch.zeros(3, 16, dtype=U8)
+    assert g.coda_add_rmsnorm(X, torch.ones(16), 1e-5, Yq=codes, scale=stale)["scale"] is stale
