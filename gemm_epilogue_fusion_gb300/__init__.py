@@ -273,6 +273,25 @@ def _stream(t: torch.Tensor, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream, device):
+    """The torch stream behind a ``stream`` argument: one of torch's, or anything with an address."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    address = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    # the default stream goes by 0 and by 1 (cudaStreamLegacy)
+    return torch.cuda.default_stream(device) if address in (0, 1) else torch.cuda.ExternalStream(address, device=device)
+
+
+def _made_on(stream, device, make):
+    """A call's own workspace, make(), from the pool of the stream it launches on.  The call drops it on return: from the
+    current stream's pool it could be given out again there, or still be in use there, while the kernels on `stream` have
+    it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(_stream_object(stream, device)):
+        return make()
+
+
 def coda_partial_cols(N: int) -> int:
     return int(load_library().coda_partial_cols(N))
 
@@ -482,8 +501,8 @@ def coda_rmsnorm_backward(dY, H, r, gamma, S, dH_in=None, dH=None, Yt=None, dgam
     if dgamma is None:
         dgamma = torch.empty(N, dtype=torch.float32, device=dY.device)
     if workspace is None:
-        n = lib.coda_rmsnorm_backward_workspace_bytes(M, N)
-        workspace = torch.empty(max(n // 4, 1), dtype=torch.float32, device=dY.device)
+        n = max(lib.coda_rmsnorm_backward_workspace_bytes(M, N) // 4, 1)
+        workspace = _made_on(stream, dY.device, lambda: torch.empty(n, dtype=torch.float32, device=dY.device))
     bf = (torch.bfloat16,)
     for t, name in ((dY, "dY"), (H, "H"), (dH_in, "dH_in"), (dH, "dH"), (Yt, "Yt")):
         _want(t, name, (M, N), bf)
@@ -986,7 +1005,7 @@ def coda_add_rmsnorm_backward(dY, H, r, gamma, dH_in=None, *, dH=None, dgamma=No
     dH = _alloc(dH, (M, N), H.dtype, H)
     dgamma = _alloc(dgamma, (N,), torch.float32, H)
     if workspace is None:
-        workspace = add_rmsnorm_backward_workspace(M, N, H.device)
+        workspace = _made_on(stream, H.device, lambda: add_rmsnorm_backward_workspace(M, N, H.device))
     if _fast is not None and _done(_fast.add_rmsnorm_backward(dY, H, r, gamma, dH_in, dH, dgamma, workspace,
                                                               _stream_arg(stream))):
         return dH, dgamma
@@ -1024,7 +1043,7 @@ def coda_route(logits, top_k: int, *, renormalize: bool = True, ids=None, weight
     offsets = _alloc(offsets, (E + 1,), torch.int32, logits)
     out = {"ids": ids, "weights": weights, "slots": slots, "offsets": offsets}
     if workspace is None:
-        workspace = route_workspace(M, E, top_k, logits.device)
+        workspace = _made_on(stream, logits.device, lambda: route_workspace(M, E, top_k, logits.device))
     if _fast is not None and _done(_fast.route(logits, ids, weights, slots, offsets, workspace, top_k, renormalize,
                                                _stream_arg(stream))):
         return out
