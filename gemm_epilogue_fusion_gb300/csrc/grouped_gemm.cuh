@@ -125,6 +125,7 @@ struct GroupCfg {
   static constexpr bool B_MN = WGRAD || BWD || PROG == kGroupPlainMN;
   static constexpr int BM = 128;
   static constexpr int TILE_M = BM;
+  static constexpr int BAND_ROWS = SWIGLU ? CODA_RASTER_ROWS_SWIGLU : CODA_RASTER_ROWS;
   static constexpr int BN = 256;
   static constexpr int STAGES = STAGES_;
   static constexpr int NSLOTS = NSLOTS_;
@@ -778,7 +779,10 @@ cudaError_t group_units(const void* kernel, int* units, const char** msg) {
   return cudaSuccess;
 }
 
-inline GroupArgs group_args(const GroupProblem& p) {
+// What a form's kernel is told of a problem: the operands, and the grid of its
+// tiles with the bands they are walked in.
+template <class C>
+GroupArgs group_args(const GroupProblem& p) {
   GroupArgs a = {};
   a.offsets = p.offsets;
   a.row_scale = p.row_scale;
@@ -789,6 +793,15 @@ inline GroupArgs group_args(const GroupProblem& p) {
   a.E = p.E;
   a.N = p.N;
   a.K = p.K;
+  if constexpr (C::WGRAD) {
+    a.m_tiles = (p.N + C::TILE_M - 1) / C::TILE_M;
+    a.n_tiles = (p.K + C::BN - 1) / C::BN;
+  } else {
+    a.n_tiles = (p.N + C::OUT_COLS - 1) / C::OUT_COLS;
+  }
+  // All of an expert's row tiles: as many as T rows have and no more, so that the band's tiles (tile_coord multiplies
+  // them out) stay below the tiles of the launch, whose number the caller has checked.
+  a.group = C::BAND_ROWS > 0 ? C::BAND_ROWS / C::TILE_M : (p.T + C::TILE_M - 1) / C::TILE_M;
   return a;
 }
 
@@ -827,10 +840,7 @@ cudaError_t launch_group_cfg(const GroupProblem& p, const char** msg) {
   if (ce != cudaSuccess) return ce;
   const int64_t bound = group_tile_bound<C>(p);
   const int grid = static_cast<int>(bound < units ? bound : units);
-  GroupArgs a = group_args(p);
-  a.m_tiles = C::WGRAD ? (p.N + C::TILE_M - 1) / C::TILE_M : 0;
-  a.n_tiles = C::WGRAD ? (p.K + C::BN - 1) / C::BN : (p.N + C::OUT_COLS - 1) / C::OUT_COLS;
-  a.group = (C::SWIGLU ? CODA_RASTER_ROWS_SWIGLU : CODA_RASTER_ROWS) / C::TILE_M;
+  GroupArgs a = group_args<C>(p);
   // an expert with one row tile reads its weight once
   a.stream_w = !C::WGRAD && p.T <= static_cast<int64_t>(p.E) * C::TILE_M;
   void* kargs[] = {&m, &a};

@@ -38,6 +38,7 @@ struct SkinnyCfg {
   static constexpr bool B_MN = BWD || PROG == kGroupPlainMN;
   static constexpr int CL = CL_;
   static constexpr int TILE_M = 32;
+  static constexpr int BAND_ROWS = 0;  // all: further row tiles follow the first one column by column, weights from L2
   static constexpr int BN = 256;
   static constexpr int STAGES = CL == 1 ? 6 : 5;
   static constexpr int ELEM = KIND == kKindBF16 ? 2 : 1;
@@ -408,9 +409,7 @@ cudaError_t launch_skinny_cfg(const GroupProblem& p, const char** msg) {
   cudaError_t ce = group_units<C, C::CL>(reinterpret_cast<const void*>(kernel), &units, msg);
   if (ce != cudaSuccess) return ce;
   const int64_t bound = group_tile_bound<C>(p);
-  GroupArgs a = group_args(p);
-  a.n_tiles = (p.N + C::OUT_COLS - 1) / C::OUT_COLS;
-  a.group = 1 << 16;  // an expert's further row tiles follow the first one column by column: its weights from L2
+  GroupArgs a = group_args<C>(p);
   a.stream_w = p.T <= C::TILE_M;
   void* kargs[] = {&m, &a};
   ce = launch_ex(reinterpret_cast<const void*>(kernel),

@@ -35,6 +35,7 @@ struct WgradCfg {
   static constexpr int CG = 2;
   static constexpr int BM = 128;
   static constexpr int TILE_M = BM * CG;
+  static constexpr int BAND_ROWS = CODA_RASTER_ROWS;
   static constexpr int HALF = 256;
   static constexpr int BN = 2 * HALF;
   static constexpr int STAGES = 3;
@@ -377,10 +378,7 @@ inline cudaError_t launch_wgrad_pairs(const GroupProblem& p, const char** msg) {
   cudaError_t ce = group_units<C, C::CG>(kernel, &units, msg);
   if (ce != cudaSuccess) return ce;
   const int64_t bound = group_tile_bound<C>(p);
-  GroupArgs a = group_args(p);
-  a.m_tiles = (p.N + C::TILE_M - 1) / C::TILE_M;
-  a.n_tiles = (p.K + C::BN - 1) / C::BN;
-  a.group = CODA_RASTER_ROWS / C::TILE_M;
+  GroupArgs a = group_args<C>(p);
   void* kargs[] = {&m, &a};
   ce = launch_ex(kernel, dim3(static_cast<unsigned>(C::CG * (bound < units ? bound : units))), dim3(C::NUM_THREADS),
                  C::SMEM_BYTES, p.stream, p.pdl, kargs, C::CG, false);

@@ -41,6 +41,7 @@ struct WideCfg {
   static constexpr int CG = 2;
   static constexpr int BM = 128;      // weight rows of a CTA
   static constexpr int TILE_M = 256;  // rows of the largest tile
+  static constexpr int BAND_ROWS = SWIGLU ? CODA_RASTER_ROWS_SWIGLU : CODA_RASTER_ROWS;
   static constexpr int STAGES = 6;
   static constexpr int ELEM = KIND == kKindBF16 ? 2 : 1;
   static constexpr int BK = 128 / ELEM;
@@ -361,9 +362,7 @@ cudaError_t launch_wide_cfg(const GroupProblem& p, const char** msg) {
   cudaError_t ce = group_units<C, C::CG>(reinterpret_cast<const void*>(kernel), &units, msg);
   if (ce != cudaSuccess) return ce;
   const int64_t bound = group_tile_bound<C>(p);
-  GroupArgs a = group_args(p);
-  a.n_tiles = (p.N + C::OUT_COLS - 1) / C::OUT_COLS;
-  a.group = (C::SWIGLU ? CODA_RASTER_ROWS_SWIGLU : CODA_RASTER_ROWS) / C::TILE_M;
+  GroupArgs a = group_args<C>(p);
   void* kargs[] = {&m, &a};
   ce = launch_ex(reinterpret_cast<const void*>(kernel), dim3(2 * static_cast<unsigned>(bound < units ? bound : units)),
                  dim3(C::NUM_THREADS), C::SMEM_BYTES, p.stream, p.pdl, kargs, C::CG, false);
