@@ -298,21 +298,6 @@ __device__ __forceinline__ void tc_fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// True in one lane of a converged warp, the same one every time.  Where one lane
-// of a warp issues MMAs, commits and TMA copies, the branch is taken by this and
-// not by a lane number: the compiler then knows that one lane is active, and
-// passes their operands on without a loop over lanes (a k-block of four MMAs
-// of a CTA pair took 0.32 us to issue, 0.19 this way).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // Arrive once on `bar` when every tcgen05.mma issued so far by this thread
 // has completed (and so has finished reading its shared-memory operands).
 // CG = 2: arrive on the mbarrier at the same offset in every CTA of `mask`.
