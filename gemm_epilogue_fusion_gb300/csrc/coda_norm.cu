@@ -159,11 +159,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const __gri
       return row_reduce<TPR, false>(ss, red);
     };
     const float n = static_cast<float>(p.N);
-    const float ss = squares(1.0f, red_sum);
-    if (ss > 0x1p126f || (p.eps == 0.0f && ss < 0x1p-80f)) {
-      // the squares of finite values leave fp32's range: summed again 2^75 times smaller or larger, which
-      // 32768 of the largest, or the smallest normal ones, do not leave (uniform over the row)
-      const float f2 = ss > 1.0f ? 0x1p-75f : 0x1p75f;
+    const float ss = squares(1.0f, red_sum), size = ss + p.eps;
+    if (size > 0x1p126f || size < 0x1p-80f) {
+      // the squares of finite values leave fp32's range, or lose their low bits at its end, beside no larger eps: summed
+      // again 2^75 times smaller or larger, which 32768 of the largest, or the smallest normal ones, do not leave
+      // (uniform over the row)
+      const float f2 = size > 1.0f ? 0x1p-75f : 0x1p75f;
       r = f2 / sqrtf(squares(f2, red_again) / n + p.eps * f2 * f2);
     } else {
       r = 1.0f / sqrtf(ss / n + p.eps);

@@ -564,7 +564,10 @@ CODA_API coda_status coda_logprobs_backward(const void* logits, int64_t ld, cons
  * are decided on the fp32 y and the correctly rounded quotient, saturating.
  * q and scale are what coda_expert_dispatch and the grouped products take; a
  * dense e4m3 GEMM takes scale as its row scale r (coda_gemm_rowscale).  A row
- * with a NaN gives NaN; with an infinity, an infinite r^-1 and NaN there. */
+ * with a NaN gives NaN; with an infinity, an infinite r^-1 and NaN there.  Any
+ * finite eps >= 0 does; where 1 / sqrt(mean h^2 + eps) is beyond fp32 (a root
+ * mean square below 2^-128 and no eps), r is infinite, and a row of zeros NaN
+ * with scale 1. */
 CODA_API coda_status coda_add_rmsnorm(const void* X, int64_t ldx, const void* R, int64_t ldr, const float* gamma,
                                       float eps, void* H, void* Y, uint8_t* q, float* scale, float* r, int64_t M,
                                       int64_t N, coda_dtype dtype, cudaStream_t stream);
