@@ -20,6 +20,7 @@
 // stores its own row), warp 1 TMEM owner and MMA issuer, warp 2 producer.
 #pragma once
 #include <cmath>
+#include <cstring>
 
 #include "grouped_gemm.cuh"
 #include "grouped_wide.cuh"
@@ -435,8 +436,12 @@ enum GroupForm { kFormPair = -2, kFormLone = -1 };
 // SwiGLU: 8.4, 10.4, 10.5, 12.5, 17, 28; 768 rows of 8 experts of 4096 x 14336,
 // SwiGLU: 287, 279, 438, 492, 601, 878, 2048 rows: 377, 459, 1173 and more; 1024
 // rows of 4 experts, 456 x 3712, SwiGLU: 19.3, 15.5, 31 and more.
+// CODA_GROUP_SPLIT=1|2|4|8 forces 32-row tiles split by that many CTAs,
+// CODA_CTA_GROUP=1|2 lone CTAs or pairs (read on every call).
 template <class Lone>
 int group_form(const GroupProblem& p) {
+  const char* split = getenv("CODA_GROUP_SPLIT");
+  if (split && split[0] && !split[1] && strchr("1248", split[0])) return split[0] - '0';
   const char* force = getenv("CODA_CTA_GROUP");
   if (force && force[0] == '1') return kFormLone;
   if (force && force[0] == '2') return kFormPair;
