@@ -1,7 +1,7 @@
 // RMSNorm as a pass of its own, with the residual's addition before it and, on
 // request, its result in e4m3 with a scale for each row; and its gradient.
 //   h = round(x + R);  r = 1 / sqrt(mean h^2 + eps);  y = h r gamma
-//   s = max_j |y_j| / 448 (1 for a row of zeros);  q = e4m3(y / s)
+//   s = max_j |y_j| / 448 (1 for a row of zeros, rounded up if subnormal);  q = e4m3(y / s)
 // Without gamma the row x itself is quantised.  Everything between the loads
 // and the stores is fp32; y is rounded once, to the output type or to a code.
 //
@@ -84,6 +84,13 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
     for (int i = 1; i < TPR / 32; ++i) v = join(v, red[i]);
   }
   return v;
+}
+
+// A row's scale: its largest value over 448 (1 for zeros).  A subnormal one is rounded up: rounded to nearest, its
+// coarse steps would leave values above 448 of them, or it would be 0, and a zero over it NaN.
+__device__ __forceinline__ float row_scale(float amax) {
+  const float s = e4m3_scale(amax);
+  return s < 0x1p-126f ? __fdiv_ru(amax, 448.0f) : s;
 }
 
 template <int N, bool FAST>
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const __gri
   }
   if (p.Yq != nullptr) {
     amax = row_reduce<TPR, true>(amax, red_max);
-    const float s = e4m3_scale(amax);
+    const float s = row_scale(amax);
     if (t == 0) p.scale[row] = s;
     const bool fast = e4m3_fast_scale(s);
     const float inv = fast ? __frcp_rn(s) : 0.0f;

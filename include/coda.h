@@ -554,7 +554,8 @@ CODA_API coda_status coda_logprobs_backward(const void* logits, int64_t ld, cons
  *   h   = X + R, rounded to dtype (h = X without R)
  *   r_i = 1 / sqrt(mean_j h_ij^2 + eps)      (of the stored h)
  *   y   = h_ij r_i gamma_j                   (fp32, then rounded once)
- *   s_i = max_j |y_ij| / 448 (1 for a row of zeros);  q_ij = e4m3(y_ij / s_i)
+ *   s_i = max_j |y_ij| / 448 (1 for a row of zeros; a subnormal one rounded
+ *         up);  q_ij = e4m3(y_ij / s_i)
  *   X, R     [M, N] dtype (CODA_F32 or CODA_BF16), rows ldx and ldr elements
  *            apart; R nullable (ldr is then not looked at)
  *   gamma    [N] fp32
