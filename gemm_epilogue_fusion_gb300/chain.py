@@ -352,16 +352,24 @@ def _experts_backward(dy, slots, offsets, Wgut, Wdt, fwd, dX_in, bufs=None):
     return {"dX": dX, "dWgut": dWgut, "dWdt": dWdt, "dGU": dGU, "dy": dy, "dxs": dxs}
 
 
+def _whole_rows(Wrt):
+    """The router's weight [E, H] with E rounded up to a multiple of 8 by rows of zeros: the logits' rows, and their
+    gradient's, are products' rows of whole 16 bytes."""
+    E = Wrt.shape[0]
+    return Wrt if E % 8 == 0 else torch.cat((Wrt, Wrt.new_zeros(-E % 8, Wrt.shape[1])))
+
+
 def moe_block(X, R, gamma, Wrt, Wgut, Wdt, eps: float, top_k: int, *, renormalize: bool = True, scale_wgu=None,
               scale_wd=None, save: bool = False, want_p: bool = False, bufs: Optional[dict] = None) -> dict:
     """A mixture-of-experts feed-forward block: h = R + X, y = RMSNorm(h), the router's choice from y Wr (Wrt [E, H]),
     and h2 = h + its experts.  With e4m3 expert weights (scale_wgu, scale_wd given) the norm also writes y's rows in
-    e4m3, and the experts read those; the router reads y in bf16 either way.  E: a multiple of 8 (the logits' rows)."""
+    e4m3, and the experts read those; the router reads y in bf16 either way.  ``bufs["logits"]``, where given, has E
+    rounded up to a multiple of 8 columns; the logits returned are its first E."""
     fp8 = scale_wgu is not None
     n = coda_add_rmsnorm(X, gamma, eps, R, H=_b(bufs, "h"), Y=_b(bufs, "yn"), Yq=_b(bufs, "yq") if fp8 else None,
                          scale=_b(bufs, "syq") if fp8 else None, r=_b(bufs, "r"), want_y=True, want_q=fp8)
     yn = n["y"]
-    logits = coda_gemm(yn, Wrt, D=_b(bufs, "logits"))
+    logits = coda_gemm(yn, _whole_rows(Wrt), D=_b(bufs, "logits"))[:, :Wrt.shape[0]]
     route = coda_route(logits, top_k, renormalize=renormalize, workspace=_b(bufs, "route_workspace"),
                        **{k: _b(bufs, k) for k in ("ids", "weights", "slots", "offsets")})
     inner = None if bufs is None else {**bufs, "h": bufs.get("h2")}
@@ -373,9 +381,16 @@ def moe_block(X, R, gamma, Wrt, Wgut, Wdt, eps: float, top_k: int, *, renormaliz
 def moe_block_backward(gamma, Wrt, Wgut, Wdt, fwd: dict, dH2, *, renormalize: bool = True) -> dict:
     """Gradients of moe_block (bf16, forward with ``save``): dX (= dR), dgamma, dWrt, dWgut, dWdt."""
     dy, dweights = coda_expert_combine_backward(dH2, fwd["y"], fwd["slots"], fwd["weights"])
-    dlogits = coda_route_backward(fwd["logits"], fwd["ids"], fwd["weights"], dweights, renormalize=renormalize)
+    E, whole = Wrt.shape[0], _whole_rows(Wrt)
+    d = dlogits = None
+    if len(whole) > E:  # the columns behind the experts' count as gradients of 0
+        d = torch.zeros(len(dH2), len(whole), dtype=Wrt.dtype, device=Wrt.device)
+        dlogits = d[:, :E]
+    dlogits = coda_route_backward(fwd["logits"], fwd["ids"], fwd["weights"], dweights, renormalize=renormalize,
+                                  dlogits=dlogits)
+    d = dlogits if d is None else d
     # the normed rows feed the router and the experts
-    e = _experts_backward(dy, fwd["slots"], fwd["offsets"], Wgut, Wdt, fwd, coda_gemm(dlogits, Wrt, b_mn=True))
+    e = _experts_backward(dy, fwd["slots"], fwd["offsets"], Wgut, Wdt, fwd, coda_gemm(d, whole, b_mn=True))
     dh, dgamma = coda_add_rmsnorm_backward(e["dX"], fwd["h"], fwd["r"], gamma, dH2)
-    return {"dX": dh, "dgamma": dgamma, "dWrt": coda_gemm(dlogits, fwd["yn"], a_mn=True, b_mn=True),
+    return {"dX": dh, "dgamma": dgamma, "dWrt": coda_gemm(d, fwd["yn"], a_mn=True, b_mn=True)[:E],
             "dWgut": e["dWgut"], "dWdt": e["dWdt"], "dlogits": dlogits}
