@@ -1422,7 +1422,7 @@ coda_status norm_impl(const char* what, const void* X, int64_t ldx, const void* 
 // Shape rules of the router calls.
 coda_status check_route(int64_t M, int64_t E, int64_t k, coda_dtype dtype) {
   REQUIRE(dtype == CODA_F32 || dtype == CODA_BF16, "dtype must be CODA_F32 or CODA_BF16");
-  REQUIRE(M >= 0 && M < INT32_MAX, "M = %" PRId64 " out of range [0, 2^31)", M);
+  REQUIRE(M >= 0 && M < coda::kMaxRouteRows, "M = %" PRId64 " out of range [0, 2^31 - 2^24)", M);
   REQUIRE(E > 0 && E <= coda::kMaxExperts, "E = %" PRId64 " out of range [1, %d]", E, coda::kMaxExperts);
   REQUIRE(k > 0 && k <= E && k <= coda::kMaxChoices, "top_k = %" PRId64 " out of range [1, min(E, %d)]", k,
           coda::kMaxChoices);
@@ -1565,7 +1565,7 @@ coda_status coda_add_rmsnorm_backward(const void* dY, const void* H, const float
 
 int64_t coda_route_workspace_bytes(int64_t M, int64_t E, int64_t top_k) {
   if (M < 0 || E <= 0 || E > coda::kMaxExperts || top_k <= 0 || top_k > coda::kMaxChoices || top_k > E ||
-      M >= INT32_MAX || M * top_k >= INT32_MAX)
+      M >= coda::kMaxRouteRows || M * top_k >= INT32_MAX)
     return -1;
   return coda::route_workspace_bytes(M, E, top_k);
 }

@@ -19,6 +19,8 @@ namespace coda {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
 constexpr int kMaxNormWidth = 32768;
+// Rows that the router takes (fewer): a block's rows, and a warp's next one, are counted in 32 bits past the last.
+constexpr int64_t kMaxRouteRows = (int64_t(1) << 31) - (1 << 24);
 
 // ------------------------------------------------------- grouped products ----
 // Programs of the grouped GEMM.  Rows [offsets[e], offsets[e + 1]) of the

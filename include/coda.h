@@ -608,8 +608,9 @@ CODA_API int64_t coda_route_workspace_bytes(int64_t M, int64_t E, int64_t top_k)
  *   offsets  [E + 1] int32
  *   workspace as above, any contents (calls that may overlap on the GPU need
  *            one each); NULL where it has 0 bytes
- * E up to 1024, top_k up to 32.  A +inf logit takes all of the weight, shared
- * among several.  All outputs are the same on every run. */
+ * E up to 1024, top_k up to 32, M below 2^31 - 2^24, M top_k below 2^31 - 1.
+ * A +inf logit takes all of the weight, shared among several.  All outputs are
+ * the same on every run. */
 CODA_API coda_status coda_route(const void* logits, int64_t ld, int64_t top_k, int renormalize, int32_t* ids,
                                 float* weights, int32_t* slots, int32_t* offsets, void* workspace, int64_t M,
                                 int64_t E, coda_dtype dtype, cudaStream_t stream);
