@@ -316,7 +316,9 @@ def expert_layer(X, slots, offsets, weights, Wgut, Wdt, R=None, *, scale_x=None,
     w_j SwiGLU_e(X) Wd_e.  Wgut [E, 2I, H] (gate rows, then up rows), Wdt [E, H, I].  bf16 in 4 launches; e4m3 operands
     (X and scale_x from coda_add_rmsnorm's q and scale, weights with scale_wgu and scale_wd [E]) in 5, act being
     quantised row by row.  ``save`` keeps G || U for the backward; ``want_p`` adds h's partial sums of squares P, for
-    the next layer's coda_gemm_*_fused_rms.  Returns xs, act, y (rows in expert order), h and what was asked for."""
+    the next layer's coda_gemm_*_fused_rms.  Returns xs, act, y (rows in expert order), h and what was asked for.
+    act and y are bf16, so y lies behind two roundings (2-norm error 0.0024, one: 0.0017) and h behind up to three; the
+    e4m3 codes are those of the bf16 act."""
     xs, sxs = coda_expert_dispatch(X, slots, scale=scale_x, Xs=_b(bufs, "xs"),
                                    scale_s=_b(bufs, "sxs") if scale_x is not None else None)
     act, GU = coda_grouped_gemm_swiglu(xs, Wgut, offsets, row_scale=sxs, w_scale=scale_wgu, Act=_b(bufs, "act"),
@@ -336,7 +338,9 @@ def expert_layer(X, slots, offsets, weights, Wgut, Wdt, R=None, *, scale_x=None,
 def expert_layer_backward(dH, slots, offsets, weights, Wgut, Wdt, fwd: dict, dX_in=None,
                           bufs: Optional[dict] = None) -> dict:
     """Gradients of expert_layer (bf16) from its saved xs, GU, act and y: dX (plus dX_in, another path's), dweights,
-    dWgut, dWdt; dR is dH itself.  6 launches."""
+    dWgut, dWdt; dR is dH itself.  6 launches.  Rows passed from call to call (dy, dGU, dxs) are bf16: dWdt lies behind
+    two roundings, dWgut behind three, dX behind four, 2-norm errors of 0.0024, 0.0029 and 0.0033 to 0.0034 (a rounding
+    adds 0.0017 in quadrature; dweights, fp32 throughout, 1e-7)."""
     dy, dweights = coda_expert_combine_backward(dH, fwd["y"], slots, weights, dY=_b(bufs, "dy"),
                                                 dweights=_b(bufs, "dweights"))
     return {**_experts_backward(dy, slots, offsets, Wgut, Wdt, fwd, dX_in, bufs), "dweights": dweights}
@@ -379,7 +383,9 @@ def moe_block(X, R, gamma, Wrt, Wgut, Wdt, eps: float, top_k: int, *, renormaliz
 
 
 def moe_block_backward(gamma, Wrt, Wgut, Wdt, fwd: dict, dH2, *, renormalize: bool = True) -> dict:
-    """Gradients of moe_block (bf16, forward with ``save``): dX (= dR), dgamma, dWrt, dWgut, dWdt."""
+    """Gradients of moe_block (bf16, forward with ``save``): dX (= dR), dgamma, dWrt, dWgut, dWdt.  The router's share of
+    the normed rows' gradient is a product's bf16 output, and added to the experts' in fp32; the roundings before that
+    are expert_layer_backward's."""
     dy, dweights = coda_expert_combine_backward(dH2, fwd["y"], fwd["slots"], fwd["weights"])
     E, whole = Wrt.shape[0], _whole_rows(Wrt)
     d = dlogits = None

@@ -15,7 +15,9 @@
 //   dh = r (gamma dy - z mean_j gamma_j dy_j z_j) + dR,  z = r h
 //   dgamma = sum over the rows of dy z
 // A block walks rows, keeping its threads' columns of dgamma in registers; a
-// second kernel adds the blocks' sums in the blocks' order.
+// second kernel adds the blocks' sums in the blocks' order.  These sums are fp32:
+// dgamma of 16384 rows of 4096 is 1.7e-7 off the 64-bit one (2-norm), where a sum
+// in 64 bits, rounded, is 3.6e-8 off.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -507,6 +509,7 @@ cudaError_t norm_pick(const NormParams& p, cudaStream_t s, bool pdl) {
 // runs at once, but six rows for each at least where that leaves every SM one
 // (the second kernel reads all their sums: 1003 rows of 2060 fp32 columns, 152
 // blocks 14.1 us, 304 14.6, 456 17.0).
+// GB300's SMs, not asked of the device: the workspace's size is told without one.
 constexpr int kNormBwdSms = 152, kNormBwdMost = 3 * kNormBwdSms;
 int norm_backward_blocks(int64_t M, int rows, int most) {
   const int64_t all = (M + rows - 1) / rows, few = all < kNormBwdSms ? all : kNormBwdSms;

@@ -276,6 +276,9 @@ struct GroupWalk {
 
 // Two columns of the SwiGLU backward, act = silu(G) U: dG = dAct U silu'(G) and
 // dU = dAct silu(G), with s = sigmoid(G) and silu'(G) = s + silu(G) (1 - s).
+// All in fp32 (the sigmoid's exponential and reciprocal are approximate, 2^-20,
+// as in the dense kernels) and rounded once, to the 16 bits that the products
+// behind it take as operands.
 __device__ __forceinline__ void group_swiglu_grad(float2 dact, uint32_t g2, uint32_t u2, uint32_t& dg2, uint32_t& du2) {
   const float2 G = make_float2(bf16_lo(g2), bf16_hi(g2));
   const float2 U = make_float2(bf16_lo(u2), bf16_hi(u2));

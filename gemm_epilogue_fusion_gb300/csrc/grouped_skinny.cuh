@@ -428,9 +428,15 @@ enum GroupForm { kFormPair = -2, kFormLone = -1 };
 // The form with the least time: rounds of tiles over what runs at once, each the
 // k-blocks' time and some for the tile's ends, or the weights' way from HBM where
 // that is longer.  The experts hit are as many as T rows hit when all are as
-// likely.  The constants fit 720 measurements (8 to 128 experts, of 4096 x 14336
-// to 1024 x 512 and 456 x 3712, 1 to 51200 rows, every form) to 10% on average;
-// the form chosen takes 3% more than the best one, 8% or more in 7 of 120.
+// likely.  The constants fit 720 bf16 measurements (4 to 128 experts, of 4096 x
+// 14336 to 1024 x 512 and 456 x 3712, 1 to 51200 rows, every form) to 10% on
+// average.  With every form of the 120 cases timed again, the one chosen takes
+// 1.7% more than the best on average, 8% or more in 9 (28% in one: 512 rows of 4
+// experts, 456 x 3712, SwiGLU).  e4m3 was not in the fit: 5.3%, 8% or more in 19
+// of 120, up to 49% where a contraction is 4 to 16 of its k-blocks long, and lone
+// CTAs often do better than the pairs taken.  The 0.21 us of a pair's k-block fits
+// tiles of few rows (their heights are not in the model); at 160 and 256 rows it
+// is 0.30 and 0.37 (grouped_wide.cuh), where pairs are the best form anyway.
 // Measured, in us, pairs, lone CTAs, and 32 rows split by 1, 2, 4 and 8: 2 rows,
 // K = 14336, N = 4096: 53, 84, 65, 43, 37, 42; 640 rows of 16 experts, 1024 x 512,
 // SwiGLU: 8.4, 10.4, 10.5, 12.5, 17, 28; 768 rows of 8 experts of 4096 x 14336,

@@ -20,6 +20,10 @@
 // ragged: SwiGLU 220 us (1570 TFLOP/s), down 130 (1330), their rows' gradient 233
 // (1480), SwiGLU's gradient 159 (1090, 830 MB of traffic).
 //
+// Sums, scales and SwiGLU are fp32; an output is rounded once, to bf16: the
+// products that follow take operands of 16 bits (or, requantised, 8), and the
+// weighted sum over a row's experts reads them with half the traffic of fp32.
+//
 // Roles: warp 0 TMA producer, 1 TMEM owner and MMA issuer (of the pair's even
 // CTA), 2..5 epilogue (SwiGLU's gradient: and 6..9).
 #pragma once
@@ -59,7 +63,8 @@ struct WideCfg {
   static constexpr int TMEM_COLS = 2 * TILE_M;
   static constexpr int NUM_EPI_THREADS = 128;  // of a group of epilogue warps
   // SwiGLU's gradient has twice the traffic of a plain product and a sigmoid: two groups of epilogue warps take its
-  // chunks in turn (64 experts of 1408 x 2048 and 469 rows: 174 -> 167 us; the other programs do not gain).
+  // chunks in turn (64 experts of 1408 x 2048 and 469 rows: 174 -> 167 us; the other programs did not gain.  Both were
+  // measured before the issue by election, when the issuer's 0.32 us a k-block could hide an epilogue).
   static constexpr int EPI_GROUPS = BWD ? 2 : 1;
   static constexpr int NUM_THREADS = 64 + EPI_GROUPS * NUM_EPI_THREADS;
   static constexpr int OFF_X = STAGES * W_BYTES;
