@@ -398,5 +398,6 @@ def moe_block_backward(gamma, Wrt, Wgut, Wdt, fwd: dict, dH2, *, renormalize: bo
     # the normed rows feed the router and the experts
     e = _experts_backward(dy, fwd["slots"], fwd["offsets"], Wgut, Wdt, fwd, coda_gemm(d, whole, b_mn=True))
     dh, dgamma = coda_add_rmsnorm_backward(e["dX"], fwd["h"], fwd["r"], gamma, dH2)
-    return {"dX": dh, "dgamma": dgamma, "dWrt": coda_gemm(d, fwd["yn"], a_mn=True, b_mn=True)[:E],
-            "dWgut": e["dWgut"], "dWdt": e["dWdt"], "dlogits": dlogits}
+    # a product over no rows is refused
+    dWrt = coda_gemm(d, fwd["yn"], a_mn=True, b_mn=True)[:E] if len(dH2) else torch.zeros_like(Wrt)
+    return {"dX": dh, "dgamma": dgamma, "dWrt": dWrt, "dWgut": e["dWgut"], "dWdt": e["dWdt"], "dlogits": dlogits}

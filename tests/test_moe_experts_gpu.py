@@ -54,3 +54,17 @@ def test_a_logits_buffer(g):
     got = b.run(chain, 2, bufs={"logits": logits})
     assert got["logits"].data_ptr() == logits.data_ptr() and torch.equal(got["logits"], want["logits"])
     assert torch.equal(got["h2"], want["h2"])
+
+
+@pytest.mark.parametrize("E", [8, 12])
+def test_no_rows(g, E):
+    """An empty batch: nothing comes out, and the weights' gradients are zeros."""
+    from gemm_epilogue_fusion_gb300 import chain
+    b = Block(0, 128, E, 64, 5)
+    f = b.run(chain, 2, save=True, want_p=True)
+    assert f["h2"].shape == (0, 128) and f["logits"].shape == (0, E) and (f["offsets"] == 0).all()
+    dH2 = torch.empty(0, 128, dtype=BF, device="cuda")
+    d = chain.moe_block_backward(b.dev["gamma"], b.dev["Wr"], b.dev["Wgu"], b.dev["Wd"], f, dH2)
+    assert d["dX"].shape == (0, 128)
+    for name, like in (("dgamma", "gamma"), ("dWrt", "Wr"), ("dWgut", "Wgu"), ("dWdt", "Wd")):
+        assert d[name].shape == b.dev[like].shape and (d[name] == 0).all(), name
