@@ -5,7 +5,10 @@ that they are contiguous CUDA tensors, passes their device pointers, sizes and
 the current CUDA stream to the C ABI function of the same name, and raises
 ``CodaError`` on a non-OK status.  All arithmetic runs in the library's
 kernels; PyTorch only provides device memory and streams.  Outputs can be
-passed in (pre-allocated) or are allocated with ``torch.empty``.
+passed in (pre-allocated) or are allocated with ``torch.empty``, on the
+current stream: a call given another ``stream`` has to be ordered with the
+current one, as for any tensor that two streams use.  A workspace that the call
+itself makes and drops is the given stream's.
 
 The library is ``libcoda_gb300.so`` next to this file, compiled for sm_103a
 by ``_build.build()``.  There is no fallback: if it cannot be built or
